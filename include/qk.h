@@ -65,7 +65,7 @@ extern "C" {
  * built with; a binding must refuse to use a library whose number differs
  * (an idea taken from the dynquant-kernels package page, "Variants": an ABI
  * number baked into the binary and checked at import). */
-#define QK_ABI_VERSION 12
+#define QK_ABI_VERSION 13
 
 typedef enum qk_status {
   QK_OK = 0,
@@ -167,6 +167,62 @@ QK_API qk_status qk_silu_mul_quant_per_token_fp8(int m, int k, const void* gate,
                                                  int64_t ld_in, qk_dtype in_dtype,
                                                  const float* scale_ub, uint8_t* q, float* scale,
                                                  qk_stream stream);
+
+/*
+ * qk_add_rmsnorm_quant_per_token / qk_add_rmsnorm_quant_per_token_fp8 --
+ * residual addition, root-mean-square norm and per-token quantisation in one
+ * kernel: the step of a decoder layer between two W8A8 products.  (No
+ * counterpart on the pages: the quantiser fused with its producer, as
+ * qk_silu_mul_quant_per_token is.)
+ *
+ * Per row, with r = x + residual rounded to x_dtype (r = x without a
+ * residual), every step binary32 RN unless said otherwise:
+ *     t     = r * weight                             (element by element)
+ *     a     = max |t|;   rstd = 1 / sqrt(mean(r^2) + eps)
+ *     z     = a * rstd;  scale = max(z, 1e-12f) / qmax     (qmax 127, or 448)
+ *             fp8 with scale_ub: scale = min(scale, *scale_ub)
+ *     inv   = qmax / a;  rstd / scale when the floor 1e-12 or the bound is
+ *             what made the scale
+ *     q     = round_half_even(t * inv)               (int8)
+ *             e4m3(clamp(t * inv, -448, 448))        (fp8)
+ *     norm_out = t * rstd, rounded to x_dtype
+ * t * rstd is the normalised row (it is not rounded to x_dtype before it is
+ * quantised) and q * scale stands for it.  rstd cancels in t * rstd / scale,
+ * so the codes do not depend on the order in which the squares are added; the
+ * scale and norm_out do, by a few units in the last place of rstd.
+ *
+ * m, k           m >= 0 (0: no-op); k > 0, k % 16 == 0
+ * x              [m, k] x_dtype, row stride ld_x elements (ld_x >= k)
+ * residual       optional [m, k] x_dtype, row stride ld_res (>= k); NULL: none
+ * weight         [k] x_dtype
+ * eps            > 0 and finite
+ * residual_out   optional [m, k] x_dtype, row stride ld_res_out (>= k): r;
+ *                needs a residual; may be residual or x itself (same pointer
+ *                and stride), and may overlap nothing else
+ * norm_out       optional [m, k] x_dtype, dense
+ * q, scale       [m, k] int8 (e4m3 codes), dense, and [m] fp32
+ * scale_ub       fp8: optional device pointer to one fp32 bound (> 0)
+ * 16-byte aligned: x, residual, weight, residual_out, norm_out, q, and every
+ * row stride * element size; scale and scale_ub 4-byte aligned.  The strides
+ * of absent tensors are ignored.
+ * Values are finite, and so are r^2 summed over the row and every t (true
+ * below 2^60 in magnitude, say); a row outside that contract gives undefined
+ * codes and scale for that row alone.
+ * Errors: QK_ERR_INVALID_ARG, QK_ERR_MISALIGNED, QK_ERR_UNSUPPORTED,
+ *         QK_ERR_CUDA.
+ */
+QK_API qk_status qk_add_rmsnorm_quant_per_token(int m, int k, const void* x, int64_t ld_x,
+                                                const void* residual, int64_t ld_res,
+                                                qk_dtype x_dtype, const void* weight, float eps,
+                                                void* residual_out, int64_t ld_res_out,
+                                                void* norm_out, int8_t* q, float* scale,
+                                                qk_stream stream);
+QK_API qk_status qk_add_rmsnorm_quant_per_token_fp8(int m, int k, const void* x, int64_t ld_x,
+                                                    const void* residual, int64_t ld_res,
+                                                    qk_dtype x_dtype, const void* weight, float eps,
+                                                    void* residual_out, int64_t ld_res_out,
+                                                    void* norm_out, const float* scale_ub,
+                                                    uint8_t* q, float* scale, qk_stream stream);
 
 /*
  * qk_w8a8_gemm -- INT8 x INT8 GEMM with INT32 accumulation and a fused
@@ -321,6 +377,94 @@ QK_API qk_status qk_w8a8_moe_gemm(int num_experts, int total_m, int n, int k, in
                                   const int32_t* expert_offsets, const int8_t* a, const int8_t* b,
                                   const float* scale_a, const float* scale_b, float output_scale,
                                   void* out, qk_dtype out_dtype, qk_stream stream);
+
+/*
+ * qk_w8a8_lora_gemm -- the shared W8A8 projection with the low-rank adapters
+ * of many requests beside it: row i of the batch uses adapter
+ * adapter_ids[i], or none when that lies outside [0, num_adapters).  (No
+ * counterpart on the pages: qk_w8a8_gemm for a server whose requests bring
+ * adapters of their own.)
+ *
+ *   s[i, r]   = lora_scale[id] * sum_k x[i, k] * lora_a[id, r, k]
+ *   d[i, j]   = sum_r s[i, r] * lora_b[id, j, r]
+ *   out[i, j] = ((((float)acc[i, j] * scale_a[i]) * scale_b[j]) * output_scale) + d[i, j]
+ * acc is exact, its scaling as in qk_w8a8_gemm; the two sums are binary32
+ * sums of exact or binary32 products in an order of the library's choice; out
+ * is rounded once.  A row without an adapter gets qk_w8a8_gemm's result bit
+ * for bit, whatever the adapters hold, and a row never sees another row's
+ * adapter.
+ *
+ * m, n, k, a, b, scale_a, scale_b, output_scale, out   as qk_w8a8_gemm with
+ *                group_k = 0 (out required)
+ * x              [m, k] x_dtype, dense, 16-B aligned: the tokens before their
+ *                quantisation (norm_out of the fused norm, say)
+ * num_adapters   >= 1
+ * rank           8 .. 128, a multiple of 8 (pad smaller ones with zeros)
+ * lora_a         [num_adapters, rank, k] bf16, 16-B aligned
+ * lora_b         [num_adapters, n, rank] bf16, 16-B aligned
+ * lora_scale     optional [num_adapters] fp32, 4-B aligned; NULL: all 1
+ * adapter_ids    [m] int32, 4-B aligned, rows in any order
+ * workspace      qk_w8a8_lora_gemm_workspace_size() bytes, 256-B aligned,
+ *                with any contents.  The call owns it until the work on
+ *                `stream` completes: calls (and captured graphs) that may
+ *                overlap need separate workspaces.
+ * Errors: those of qk_w8a8_gemm.
+ */
+QK_API qk_status qk_w8a8_lora_gemm(int m, int n, int k, const int8_t* a, const int8_t* b,
+                                   const float* scale_a, const float* scale_b, float output_scale,
+                                   const void* x, qk_dtype x_dtype, int num_adapters, int rank,
+                                   const void* lora_a, const void* lora_b, const float* lora_scale,
+                                   const int32_t* adapter_ids, void* out, qk_dtype out_dtype,
+                                   void* workspace, size_t workspace_bytes, qk_stream stream);
+
+/* Bytes of workspace qk_w8a8_lora_gemm needs on the current device (0 for
+ * arguments it would reject and for empty outputs). */
+QK_API size_t qk_w8a8_lora_gemm_workspace_size(int m, int n, int k, int rank);
+
+/*
+ * qk_w8a8_moe_layer -- a whole W8A8 mixture-of-experts layer for a few
+ * tokens: the gate and up products, silu(gate) * up, its quantisation, the
+ * down product and the weighted sum over each token's experts, from the
+ * tokens in their own order and the router's choice.  (No counterpart on the
+ * pages beyond qk_w8a8_moe_gemm's, which wants tokens grouped by expert and
+ * serves larger batches.)
+ *
+ * For token i and slot s, e = topk_ids[i, s]:
+ *   g, u  = ((float)acc * scale_a[i]) * scale_gate_up[e, row]   (rows j, inter + j)
+ *   h     = silu(g) * u, as qk_silu_mul_quant_per_token forms it
+ *   q, sh = h quantised per (token, slot), as qk_quantize_per_token
+ *   y     = ((float)acc2 * sh) * scale_down[e, j]
+ *   out[i, j]: f = 0; for s = 0, 1, ...: f = fmaf(topk_weights[i, s], y, f)
+ * rounded once to out_dtype.  A slot whose id lies outside [0, num_experts)
+ * (an expert of another rank: -1) adds nothing; a token without experts gets
+ * zeros.  The same expert in two slots counts twice.  The result does not
+ * depend on what else is in the batch.
+ *
+ * m              tokens, 0 .. 64 (0: no-op; more: QK_ERR_UNSUPPORTED)
+ * hidden, inter  > 0, multiples of 16, <= 133144 (QK_ERR_OVERFLOW_BOUND)
+ * num_experts    1 .. 1024;  topk  1 .. 32 (more: QK_ERR_UNSUPPORTED)
+ * a, scale_a     [m, hidden] int8, 16-B aligned, and [m] fp32
+ * topk_ids, topk_weights   [m, topk] int32 and fp32, 4-B aligned
+ * w_gate_up      [num_experts, 2 * inter, hidden] int8: an expert's gate rows,
+ *                then its up rows; scale_gate_up [num_experts, 2 * inter] fp32
+ * w_down         [num_experts, hidden, inter] int8; scale_down
+ *                [num_experts, hidden] fp32
+ * out            [m, hidden] out_dtype
+ * workspace      qk_w8a8_moe_layer_workspace_size() bytes, 256-B aligned, with
+ *                any contents; owned by the call as for qk_w8a8_lora_gemm
+ * Alignment: 16 bytes for a, the weights and out, 4 for the scales.
+ * Errors: QK_ERR_INVALID_ARG, QK_ERR_MISALIGNED, QK_ERR_OVERFLOW_BOUND,
+ *         QK_ERR_WORKSPACE, QK_ERR_UNSUPPORTED, QK_ERR_CUDA.
+ */
+QK_API qk_status qk_w8a8_moe_layer(int m, int hidden, int inter, int num_experts, int topk,
+                                   const int8_t* a, const float* scale_a, const int32_t* topk_ids,
+                                   const float* topk_weights, const int8_t* w_gate_up,
+                                   const float* scale_gate_up, const int8_t* w_down,
+                                   const float* scale_down, void* out, qk_dtype out_dtype,
+                                   void* workspace, size_t workspace_bytes, qk_stream stream);
+
+/* Bytes of workspace qk_w8a8_moe_layer needs (0 for sizes it would reject). */
+QK_API size_t qk_w8a8_moe_layer_workspace_size(int m, int hidden, int inter, int topk);
 
 /*
  * qk_quantize_static -- static per-tensor INT8 ("write-int8-quantized-

@@ -13,7 +13,10 @@
 
 #include "gemm_sm100.cuh"
 #include "gemv.cuh"
+#include "lora.cuh"
 #include "mma_probe.cuh"
+#include "moe_layer.cuh"
+#include "norm.cuh"
 #include "qk_common.cuh"
 #include "quant.cuh"
 
@@ -246,6 +249,70 @@ qk_status qk_silu_mul_quant_per_token_fp8(int m, int k, const void* gate, const 
                                           uint8_t* q, float* scale, qk_stream stream) {
   return quant_common(m, k, gate, up, ld_in, in_dtype, reinterpret_cast<int8_t*>(q), scale,
                       stream, true, true, scale_ub);
+}
+
+namespace {
+qk_status norm_common(int m, int k, const void* x, int64_t ld_x, const void* residual, int64_t ld_res,
+                      qk_dtype dt, const void* weight, float eps, void* residual_out, int64_t ld_res_out,
+                      void* norm_out, int8_t* q, float* scale, qk_stream stream, bool fp8, const float* ub) {
+  if (m < 0 || k <= 0 || (k % 16) != 0) return QK_ERR_INVALID_ARG;
+  if (dt != QK_F32 && dt != QK_BF16) return QK_ERR_INVALID_ARG;
+  if (!(eps > 0.0f) || !(eps <= 3.402823466e38f)) return QK_ERR_INVALID_ARG;
+  if (ld_x < k || (residual != nullptr && ld_res < k) || (residual_out != nullptr && ld_res_out < k))
+    return QK_ERR_INVALID_ARG;
+  if (m == 0) return QK_OK;
+  if (x == nullptr || weight == nullptr || q == nullptr || scale == nullptr ||
+      (residual_out != nullptr && residual == nullptr))
+    return QK_ERR_INVALID_ARG;
+  const int64_t esize = dt == QK_BF16 ? 2 : 4;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(residual_out, 16) ||
+      !aligned(norm_out, 16) || !aligned(q, 16) || !aligned(scale, 4) || !aligned(ub, 4) ||
+      (ld_x * esize) % 16 != 0 || (residual != nullptr && (ld_res * esize) % 16 != 0) ||
+      (residual_out != nullptr && (ld_res_out * esize) % 16 != 0))
+    return QK_ERR_MISALIGNED;
+  // in place means the same rows: another stride would write rows not read yet
+  if (residual_out != nullptr &&
+      ((residual_out == x && ld_res_out != ld_x) || (residual_out == residual && ld_res_out != ld_res)))
+    return QK_ERR_INVALID_ARG;
+  const DeviceInfo* dev = nullptr;
+  const qk_status st = check_device(&dev);
+  if (st != QK_OK) return st;
+  norm::Args a = {};
+  a.m = m;
+  a.k = k;
+  a.x = x;
+  a.ldx = ld_x;
+  a.res = residual;
+  a.ldr = ld_res;
+  a.res_out = residual_out;
+  a.ldo = ld_res_out;
+  a.w = weight;
+  a.eps = eps;
+  a.y = norm_out;
+  a.q = q;
+  a.scale = scale;
+  a.fp8 = fp8 ? 1 : 0;
+  a.ub = fp8 ? ub : nullptr;
+  return cuda_status(norm::launch(a, dt == QK_BF16, dev->sms, reinterpret_cast<cudaStream_t>(stream)),
+                     "norm quantize launch");
+}
+}  // namespace
+
+qk_status qk_add_rmsnorm_quant_per_token(int m, int k, const void* x, int64_t ld_x, const void* residual,
+                                         int64_t ld_res, qk_dtype x_dtype, const void* weight, float eps,
+                                         void* residual_out, int64_t ld_res_out, void* norm_out, int8_t* q,
+                                         float* scale, qk_stream stream) {
+  return norm_common(m, k, x, ld_x, residual, ld_res, x_dtype, weight, eps, residual_out, ld_res_out,
+                     norm_out, q, scale, stream, false, nullptr);
+}
+
+qk_status qk_add_rmsnorm_quant_per_token_fp8(int m, int k, const void* x, int64_t ld_x, const void* residual,
+                                             int64_t ld_res, qk_dtype x_dtype, const void* weight, float eps,
+                                             void* residual_out, int64_t ld_res_out, void* norm_out,
+                                             const float* scale_ub, uint8_t* q, float* scale,
+                                             qk_stream stream) {
+  return norm_common(m, k, x, ld_x, residual, ld_res, x_dtype, weight, eps, residual_out, ld_res_out,
+                     norm_out, reinterpret_cast<int8_t*>(q), scale, stream, true, scale_ub);
 }
 
 namespace {
@@ -592,6 +659,171 @@ size_t qk_w8a8_linear_workspace_size(int m, int n, int k, int group_k) {
   const size_t g = round256(qk_w8a8_gemm_workspace_size(m, n, k, group_k));
   return g + kLinearFlagBytes + round256(static_cast<size_t>(m) * static_cast<size_t>(k)) +
          round256(static_cast<size_t>(m) * 4);
+}
+
+// ---- adapters beside the projection; the workspace holds the GEMM's own
+// part, then s [m, rank], then the int32 sums [m, n]
+namespace {
+struct LoraLayout {
+  size_t gemm, s, c, total;
+};
+
+LoraLayout lora_layout(int m, int n, int k, int rank) {
+  LoraLayout l;
+  l.gemm = round256(qk_w8a8_gemm_workspace_size(m, n, k, 0));
+  l.s = round256(static_cast<size_t>(m) * rank * 4);
+  l.c = round256(static_cast<size_t>(m) * static_cast<size_t>(n) * 4);
+  l.total = l.gemm + l.s + l.c;
+  return l;
+}
+
+qk_status lora_check(int m, int n, int k, int rank) {
+  const qk_status st = gemm_check(m, n, k, 0);
+  if (st != QK_OK) return st;
+  return (rank < 8 || rank > 128 || (rank % 8) != 0) ? QK_ERR_INVALID_ARG : QK_OK;
+}
+}  // namespace
+
+size_t qk_w8a8_lora_gemm_workspace_size(int m, int n, int k, int rank) {
+  if (lora_check(m, n, k, rank) != QK_OK || m == 0 || n == 0) return 0;
+  return lora_layout(m, n, k, rank).total;
+}
+
+qk_status qk_w8a8_lora_gemm(int m, int n, int k, const int8_t* a, const int8_t* b, const float* scale_a,
+                            const float* scale_b, float output_scale, const void* x, qk_dtype x_dtype,
+                            int num_adapters, int rank, const void* lora_a, const void* lora_b,
+                            const float* lora_scale, const int32_t* adapter_ids, void* out,
+                            qk_dtype out_dtype, void* workspace, size_t workspace_bytes, qk_stream stream) {
+  qk_status st = lora_check(m, n, k, rank);
+  if (st != QK_OK) return st;
+  if (num_adapters < 1) return QK_ERR_INVALID_ARG;
+  if (x_dtype != QK_F32 && x_dtype != QK_BF16) return QK_ERR_INVALID_ARG;
+  if (out_dtype != QK_F32 && out_dtype != QK_BF16) return QK_ERR_INVALID_ARG;
+  if (m == 0 || n == 0) return QK_OK;
+  if (a == nullptr || b == nullptr || scale_a == nullptr || scale_b == nullptr || x == nullptr ||
+      lora_a == nullptr || lora_b == nullptr || adapter_ids == nullptr || out == nullptr)
+    return QK_ERR_INVALID_ARG;
+  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(scale_a, 16) || !aligned(scale_b, 16) ||
+      !aligned(x, 16) || !aligned(lora_a, 16) || !aligned(lora_b, 16) || !aligned(lora_scale, 4) ||
+      !aligned(adapter_ids, 4) || !aligned(out, 16))
+    return QK_ERR_MISALIGNED;
+  const DeviceInfo* dev = nullptr;
+  st = check_device(&dev);
+  if (st != QK_OK) return st;
+  const LoraLayout l = lora_layout(m, n, k, rank);
+  if (workspace == nullptr || workspace_bytes < l.total || !aligned(workspace, 256)) return QK_ERR_WORKSPACE;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  lora::Args la = {};
+  la.m = m;
+  la.n = n;
+  la.k = k;
+  la.rank = rank;
+  la.adapters = num_adapters;
+  la.x = x;
+  la.la = static_cast<const __nv_bfloat16*>(lora_a);
+  la.lb = static_cast<const __nv_bfloat16*>(lora_b);
+  la.lscale = lora_scale;
+  la.ids = adapter_ids;
+  la.sa = scale_a;
+  la.sw = scale_b;
+  la.alpha = output_scale;
+  la.s = reinterpret_cast<float*>(ws + l.gemm);
+  la.c = reinterpret_cast<const int32_t*>(ws + l.gemm + l.s);
+  la.out = out;
+  la.out_bf16 = out_dtype == QK_BF16;
+  // the GEMM's counters and split-K accumulators start at zero
+  gemm::PairPlan pl;
+  if (l.gemm > 0 && pair_plan_for(m, n, k, 0, &pl) &&
+      cudaMemsetAsync(workspace, 0, gemm::pair_workspace_zero_bytes(pl), s) != cudaSuccess)
+    return QK_ERR_CUDA;
+  st = cuda_status(lora::launch_shrink(la, x_dtype == QK_BF16, s), "adapter shrink launch");
+  if (st != QK_OK) return st;
+  st = gemm_common(m, n, k, a, b, scale_a, scale_b, 0, output_scale, const_cast<int32_t*>(la.c), nullptr,
+                   out_dtype, l.gemm > 0 ? workspace : nullptr, l.gemm, stream, nullptr, nullptr);
+  if (st != QK_OK) return st;
+  return cuda_status(lora::launch_expand(la, dev->sms, s), "adapter expand launch");
+}
+
+// ---- a MoE layer for a few tokens; the workspace holds h, y, the scales of
+// h and its int8 values
+namespace {
+constexpr int kMoeLayerTokens = 64, kMoeLayerTopk = 32, kMoeLayerExperts = 1024;
+
+struct MoeLayout {
+  size_t h, y, sh, q, total;  // byte offsets
+};
+
+MoeLayout moe_layout(int m, int hidden, int inter, int topk) {
+  const size_t pairs = static_cast<size_t>(m) * topk;
+  MoeLayout l;
+  l.h = 0;
+  l.y = l.h + round256(pairs * inter * 4);
+  l.sh = l.y + round256(pairs * hidden * 4);
+  l.q = l.sh + round256(pairs * 4);
+  l.total = l.q + round256(pairs * inter);
+  return l;
+}
+
+qk_status moe_layer_check(int m, int hidden, int inter, int topk) {
+  if (m < 0 || hidden <= 0 || inter <= 0 || (hidden % 16) != 0 || (inter % 16) != 0 || topk < 1)
+    return QK_ERR_INVALID_ARG;
+  if (hidden > kMaxK || inter > kMaxK) return QK_ERR_OVERFLOW_BOUND;
+  return (m > kMoeLayerTokens || topk > kMoeLayerTopk) ? QK_ERR_UNSUPPORTED : QK_OK;
+}
+}  // namespace
+
+size_t qk_w8a8_moe_layer_workspace_size(int m, int hidden, int inter, int topk) {
+  if (moe_layer_check(m, hidden, inter, topk) != QK_OK || m == 0) return 0;
+  return moe_layout(m, hidden, inter, topk).total;
+}
+
+qk_status qk_w8a8_moe_layer(int m, int hidden, int inter, int num_experts, int topk, const int8_t* a,
+                            const float* scale_a, const int32_t* topk_ids, const float* topk_weights,
+                            const int8_t* w_gate_up, const float* scale_gate_up, const int8_t* w_down,
+                            const float* scale_down, void* out, qk_dtype out_dtype, void* workspace,
+                            size_t workspace_bytes, qk_stream stream) {
+  qk_status st = moe_layer_check(m, hidden, inter, topk);
+  if (st != QK_OK) return st;
+  if (num_experts < 1) return QK_ERR_INVALID_ARG;
+  if (num_experts > kMoeLayerExperts) return QK_ERR_UNSUPPORTED;
+  if (out_dtype != QK_F32 && out_dtype != QK_BF16) return QK_ERR_INVALID_ARG;
+  if (m == 0) return QK_OK;
+  if (a == nullptr || scale_a == nullptr || topk_ids == nullptr || topk_weights == nullptr ||
+      w_gate_up == nullptr || scale_gate_up == nullptr || w_down == nullptr || scale_down == nullptr ||
+      out == nullptr)
+    return QK_ERR_INVALID_ARG;
+  if (!aligned(a, 16) || !aligned(w_gate_up, 16) || !aligned(w_down, 16) || !aligned(out, 16) ||
+      !aligned(scale_a, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) ||
+      !aligned(scale_gate_up, 4) || !aligned(scale_down, 4))
+    return QK_ERR_MISALIGNED;
+  const DeviceInfo* dev = nullptr;
+  st = check_device(&dev);
+  if (st != QK_OK) return st;
+  const MoeLayout l = moe_layout(m, hidden, inter, topk);
+  if (workspace == nullptr || workspace_bytes < l.total || !aligned(workspace, 256)) return QK_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  moe::Args g = {};
+  g.m = m;
+  g.hidden = hidden;
+  g.inter = inter;
+  g.experts = num_experts;
+  g.topk = topk;
+  g.a = a;
+  g.sa = scale_a;
+  g.ids = topk_ids;
+  g.wt = topk_weights;
+  g.w13 = w_gate_up;
+  g.s13 = scale_gate_up;
+  g.w2 = w_down;
+  g.s2 = scale_down;
+  g.h = reinterpret_cast<float*>(ws + l.h);
+  g.y = reinterpret_cast<float*>(ws + l.y);
+  g.sh = reinterpret_cast<float*>(ws + l.sh);
+  g.q = reinterpret_cast<int8_t*>(ws + l.q);
+  g.out = out;
+  g.out_bf16 = out_dtype == QK_BF16;
+  return cuda_status(moe::launch(g, dev->sms, reinterpret_cast<cudaStream_t>(stream)), "moe layer launch");
 }
 
 qk_status qk_w8a8_linear(int m, int n, int k, const void* x, qk_dtype x_dtype, const int8_t* b,

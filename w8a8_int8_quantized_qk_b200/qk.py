@@ -23,7 +23,7 @@ import os
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libqk.so")
 
-ABI_VERSION = 12
+ABI_VERSION = 13
 
 QK_OK = 0
 QK_ERR_INVALID_ARG = 1
@@ -54,6 +54,12 @@ _SIGNATURES = {
                                                  _P]),
     "qk_silu_mul_quant_per_token_fp8": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _P, _P, ctypes.c_int64,
                                                        ctypes.c_int, _P, _P, _P, _P]),
+    "qk_add_rmsnorm_quant_per_token": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _P, ctypes.c_int64, _P,
+                                                      ctypes.c_int64, ctypes.c_int, _P, ctypes.c_float, _P,
+                                                      ctypes.c_int64, _P, _P, _P, _P]),
+    "qk_add_rmsnorm_quant_per_token_fp8": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _P, ctypes.c_int64, _P,
+                                                          ctypes.c_int64, ctypes.c_int, _P, ctypes.c_float, _P,
+                                                          ctypes.c_int64, _P, _P, _P, _P, _P]),
     "qk_w8a8_gemm": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, _P, _P, _P, ctypes.c_int,
                                     ctypes.c_float, _P, _P, ctypes.c_int, _P, ctypes.c_size_t, _P]),
     "qk_fp8_gemm": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, _P, _P, _P, ctypes.c_float,
@@ -62,6 +68,16 @@ _SIGNATURES = {
                                                   _P]),
     "qk_w8a8_moe_gemm": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                         _P, _P, _P, _P, _P, ctypes.c_float, _P, ctypes.c_int, _P]),
+    "qk_w8a8_lora_gemm": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, _P, _P, _P, ctypes.c_float,
+                                         _P, ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, _P, _P, _P, _P,
+                                         ctypes.c_int, _P, ctypes.c_size_t, _P]),
+    "qk_w8a8_lora_gemm_workspace_size": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                                           ctypes.c_int]),
+    "qk_w8a8_moe_layer": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                         _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int, _P, ctypes.c_size_t,
+                                         _P]),
+    "qk_w8a8_moe_layer_workspace_size": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                                           ctypes.c_int]),
     "qk_quantize_static": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _P, ctypes.c_int, _P, _P, _P]),
     "qk_weight_row_sums": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _P, _P, _P]),
     "qk_w8a8_gemm_asym": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, _P, _P, _P, _P, _P,
@@ -144,6 +160,19 @@ def qk_silu_mul_quant_per_token_fp8(m, k, gate, up, ld_in, in_dtype, scale_ub, q
                                                  stream)
 
 
+def qk_add_rmsnorm_quant_per_token(m, k, x, ld_x, residual, ld_res, x_dtype, weight, eps, residual_out,
+                                   ld_res_out, norm_out, q, scale, stream) -> int:
+    return lib().qk_add_rmsnorm_quant_per_token(m, k, x, ld_x, residual, ld_res, x_dtype, weight, eps,
+                                                residual_out, ld_res_out, norm_out, q, scale, stream)
+
+
+def qk_add_rmsnorm_quant_per_token_fp8(m, k, x, ld_x, residual, ld_res, x_dtype, weight, eps, residual_out,
+                                       ld_res_out, norm_out, scale_ub, q, scale, stream) -> int:
+    return lib().qk_add_rmsnorm_quant_per_token_fp8(m, k, x, ld_x, residual, ld_res, x_dtype, weight, eps,
+                                                    residual_out, ld_res_out, norm_out, scale_ub, q, scale,
+                                                    stream)
+
+
 def qk_w8a8_gemm(m, n, k, a, b, scale_a, scale_b, group_k, output_scale, c, out, out_dtype,
                  workspace, workspace_bytes, stream) -> int:
     return lib().qk_w8a8_gemm(m, n, k, a, b, scale_a, scale_b, group_k, output_scale, c, out,
@@ -162,6 +191,30 @@ def qk_w8a8_moe_gemm(num_experts, total_m, n, k, max_m_per_expert, expert_offset
                      output_scale, out, out_dtype, stream) -> int:
     return lib().qk_w8a8_moe_gemm(num_experts, total_m, n, k, max_m_per_expert, expert_offsets, a, b,
                                   scale_a, scale_b, output_scale, out, out_dtype, stream)
+
+
+def qk_w8a8_lora_gemm(m, n, k, a, b, scale_a, scale_b, output_scale, x, x_dtype, num_adapters, rank, lora_a,
+                      lora_b, lora_scale, adapter_ids, out, out_dtype, workspace, workspace_bytes,
+                      stream) -> int:
+    return lib().qk_w8a8_lora_gemm(m, n, k, a, b, scale_a, scale_b, output_scale, x, x_dtype, num_adapters,
+                                   rank, lora_a, lora_b, lora_scale, adapter_ids, out, out_dtype, workspace,
+                                   workspace_bytes, stream)
+
+
+def qk_w8a8_lora_gemm_workspace_size(m, n, k, rank) -> int:
+    return lib().qk_w8a8_lora_gemm_workspace_size(m, n, k, rank)
+
+
+def qk_w8a8_moe_layer(m, hidden, inter, num_experts, topk, a, scale_a, topk_ids, topk_weights, w_gate_up,
+                      scale_gate_up, w_down, scale_down, out, out_dtype, workspace, workspace_bytes,
+                      stream) -> int:
+    return lib().qk_w8a8_moe_layer(m, hidden, inter, num_experts, topk, a, scale_a, topk_ids, topk_weights,
+                                   w_gate_up, scale_gate_up, w_down, scale_down, out, out_dtype, workspace,
+                                   workspace_bytes, stream)
+
+
+def qk_w8a8_moe_layer_workspace_size(m, hidden, inter, topk) -> int:
+    return lib().qk_w8a8_moe_layer_workspace_size(m, hidden, inter, topk)
 
 
 def qk_quantize_static(m, k, x, x_dtype, scale, q, stream) -> int:
@@ -507,6 +560,205 @@ def w8a8_linear_fused(x, w_q, sw, output_scale: float = 1.0, out_dtype=None, wan
                                 _stream(stream)),
            "qk_w8a8_linear_fused")
     return out, sa
+
+
+# The helpers below allocate on the stream they launch on (so a workspace that
+# is dropped on return is not handed out before the kernels have run) and on
+# the tensors' own device.
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _same_device(x, *ts) -> None:
+    _need_cuda(x, *ts)
+    for t in ts:
+        if t is not None and t.device != x.device:
+            raise ValueError(f"tensors on {x.device} and {t.device}: one device is needed")
+
+
+class _On:
+    """Makes `device` current, and `stream` (a torch stream, or None for the
+    current one) the stream that torch allocates for; .ptr is its handle."""
+
+    __slots__ = ("ctx", "ptr")
+
+    def __init__(self, device, stream):
+        torch = _torch()
+        self.ctx = None
+        if stream is not None:
+            _need(stream.device == device, f"stream of {stream.device}, tensors on {device}")
+            self.ctx = torch.cuda.stream(stream)
+        elif device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        self.ptr = _torch().cuda.current_stream().cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _matrix(t, shape, dtype, what, dense=True):
+    """Checks a tensor's type, shape and layout (dense, or rows of any stride)."""
+    _need(t.dtype == dtype, f"{what}: expected {dtype}, got {t.dtype}")
+    _need(tuple(t.shape) == shape, f"{what}: expected shape {shape}, got {tuple(t.shape)}")
+    if dense:
+        _need(t.is_contiguous(), f"{what}: must be contiguous")
+    else:
+        _need(t.stride(-1) == 1 or shape[-1] == 1, f"{what}: the last dimension must be contiguous")
+
+
+def _row_stride(t) -> int:
+    """Row stride of a matrix in elements (a single row's own length)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _rmsnorm_quant(x, weight, residual, eps, scale_ub, want_norm, residual_out, norm_out, q, scale, stream, fp8):
+    torch = _torch()
+    _same_device(x, weight, residual, scale_ub, residual_out, norm_out, q, scale)
+    _need(x.dim() == 2, f"x: expected [m, k], got {tuple(x.shape)}")
+    m, k = shape = tuple(x.shape)
+    dt, code = x.dtype, _dtype_code(x)
+    codes = torch.uint8 if fp8 else torch.int8
+    _matrix(x, shape, dt, "x", dense=False)
+    _matrix(weight, (k,), dt, "weight")
+    _need(residual is not None or residual_out is None, "residual_out: needs a residual")
+    if residual is not None:
+        _matrix(residual, shape, dt, "residual", dense=False)
+    if scale_ub is not None:
+        _matrix(scale_ub, (1,), torch.float32, "scale_ub")
+    with _On(x.device, stream) as on:
+        if residual_out is not None:
+            _matrix(residual_out, shape, dt, "residual_out", dense=False)
+        elif residual is not None:
+            residual_out = torch.empty(shape, dtype=dt, device=x.device)
+        if norm_out is not None:
+            _matrix(norm_out, shape, dt, "norm_out")
+        elif want_norm:
+            norm_out = torch.empty(shape, dtype=dt, device=x.device)
+        if q is None:
+            q = torch.empty(shape, dtype=codes, device=x.device)
+        else:
+            _matrix(q, shape, codes, "q")
+        if scale is None:
+            scale = torch.empty((m,), dtype=torch.float32, device=x.device)
+        else:
+            _matrix(scale, (m,), torch.float32, "scale")
+        head = (m, k, x.data_ptr(), _row_stride(x), _addr(residual), _row_stride(residual) if residual is not None
+                else 0, code, weight.data_ptr(), float(eps), _addr(residual_out),
+                _row_stride(residual_out) if residual_out is not None else 0, _addr(norm_out))
+        if fp8:
+            _check(qk_add_rmsnorm_quant_per_token_fp8(*head, _addr(scale_ub), q.data_ptr(), scale.data_ptr(), on.ptr),
+                   "qk_add_rmsnorm_quant_per_token_fp8")
+        else:
+            _check(qk_add_rmsnorm_quant_per_token(*head, q.data_ptr(), scale.data_ptr(), on.ptr),
+                   "qk_add_rmsnorm_quant_per_token")
+    return q, scale, residual_out, norm_out
+
+
+def add_rmsnorm_quant_per_token(x, weight, residual=None, eps: float = 1e-6, want_norm: bool = False,
+                                residual_out=None, norm_out=None, q=None, scale=None, stream=None):
+    """x [m, k] bf16/fp32 (rows of any stride), weight [k], residual [m, k] or None ->
+    (q int8 [m, k], scale fp32 [m], x + residual or None, the normalised rows or None).
+    residual_out may be `residual` or `x` (in place); a new tensor by default."""
+    return _rmsnorm_quant(x, weight, residual, eps, None, want_norm, residual_out, norm_out, q, scale, stream,
+                          False)
+
+
+def add_rmsnorm_quant_per_token_fp8(x, weight, residual=None, eps: float = 1e-6, scale_ub=None,
+                                    want_norm: bool = False, residual_out=None, norm_out=None, q=None, scale=None,
+                                    stream=None):
+    """add_rmsnorm_quant_per_token with e4m3 codes (uint8) and an optional one-element
+    bound of the scales."""
+    return _rmsnorm_quant(x, weight, residual, eps, scale_ub, want_norm, residual_out, norm_out, q, scale, stream,
+                          True)
+
+
+def w8a8_lora_gemm(a, b, scale_a, scale_b, x, lora_a, lora_b, adapter_ids, lora_scale=None,
+                   output_scale: float = 1.0, out_dtype=None, out=None, workspace=None, stream=None):
+    """a int8 [m, k], b int8 [n, k], x [m, k] bf16/fp32 (the tokens before quantisation),
+    lora_a bf16 [adapters, rank, k], lora_b bf16 [adapters, n, rank], adapter_ids int32 [m]
+    (-1: none), lora_scale fp32 [adapters] or None -> out [m, n]."""
+    torch = _torch()
+    _same_device(a, b, scale_a, scale_b, x, lora_a, lora_b, adapter_ids, lora_scale, out, workspace)
+    _need(a.dim() == 2 and b.dim() == 2, "a and b: expected [m, k] and [n, k]")
+    _need(lora_a.dim() == 3, "lora_a: expected [adapters, rank, k]")
+    m, k = a.shape
+    n = b.shape[0]
+    adapters, rank = lora_a.shape[:2]
+    _matrix(a, (m, k), torch.int8, "a")
+    _matrix(b, (n, k), torch.int8, "b")
+    _matrix(scale_a, (m,), torch.float32, "scale_a")
+    _matrix(scale_b, (n,), torch.float32, "scale_b")
+    _matrix(x, (m, k), x.dtype, "x")
+    _matrix(lora_a, (adapters, rank, k), torch.bfloat16, "lora_a")
+    _matrix(lora_b, (adapters, n, rank), torch.bfloat16, "lora_b")
+    _matrix(adapter_ids, (m,), torch.int32, "adapter_ids")
+    if lora_scale is not None:
+        _matrix(lora_scale, (adapters,), torch.float32, "lora_scale")
+    x_code = _dtype_code(x)
+    with _On(a.device, stream) as on:
+        if out is None:
+            out = torch.empty((m, n), dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=a.device)
+        else:
+            _matrix(out, (m, n), out.dtype if out_dtype is None else out_dtype, "out")
+        need = qk_w8a8_lora_gemm_workspace_size(m, n, k, rank)
+        if need and workspace is None:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=a.device)
+        _check(qk_w8a8_lora_gemm(m, n, k, a.data_ptr(), b.data_ptr(), scale_a.data_ptr(), scale_b.data_ptr(),
+                                 float(output_scale), x.data_ptr(), x_code, adapters, rank, lora_a.data_ptr(),
+                                 lora_b.data_ptr(), _addr(lora_scale), adapter_ids.data_ptr(), out.data_ptr(),
+                                 _dtype_code(out), _addr(workspace),
+                                 0 if workspace is None else workspace.numel() * workspace.element_size(), on.ptr),
+               "qk_w8a8_lora_gemm")
+    return out
+
+
+def w8a8_moe_layer(a, scale_a, topk_ids, topk_weights, w_gate_up, scale_gate_up, w_down, scale_down,
+                   out_dtype=None, out=None, workspace=None, stream=None):
+    """a int8 [m, hidden] (m <= 64), topk_ids int32 and topk_weights fp32 [m, topk],
+    w_gate_up int8 [experts, 2 inter, hidden], w_down int8 [experts, hidden, inter] and their
+    per-channel scales -> out [m, hidden]."""
+    torch = _torch()
+    _same_device(a, scale_a, topk_ids, topk_weights, w_gate_up, scale_gate_up, w_down, scale_down, out, workspace)
+    _need(a.dim() == 2 and topk_ids.dim() == 2, "a and topk_ids: expected [m, hidden] and [m, topk]")
+    _need(w_down.dim() == 3, "w_down: expected [experts, hidden, inter]")
+    m, hidden = a.shape
+    topk = topk_ids.shape[1]
+    experts, _, inter = w_down.shape
+    _matrix(a, (m, hidden), torch.int8, "a")
+    _matrix(scale_a, (m,), torch.float32, "scale_a")
+    _matrix(topk_ids, (m, topk), torch.int32, "topk_ids")
+    _matrix(topk_weights, (m, topk), torch.float32, "topk_weights")
+    _matrix(w_gate_up, (experts, 2 * inter, hidden), torch.int8, "w_gate_up")
+    _matrix(scale_gate_up, (experts, 2 * inter), torch.float32, "scale_gate_up")
+    _matrix(w_down, (experts, hidden, inter), torch.int8, "w_down")
+    _matrix(scale_down, (experts, hidden), torch.float32, "scale_down")
+    with _On(a.device, stream) as on:
+        if out is None:
+            out = torch.empty((m, hidden), dtype=torch.bfloat16 if out_dtype is None else out_dtype,
+                              device=a.device)
+        else:
+            _matrix(out, (m, hidden), out.dtype if out_dtype is None else out_dtype, "out")
+        need = qk_w8a8_moe_layer_workspace_size(m, hidden, inter, topk)
+        if need and workspace is None:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=a.device)
+        _check(qk_w8a8_moe_layer(m, hidden, inter, experts, topk, a.data_ptr(), scale_a.data_ptr(),
+                                 topk_ids.data_ptr(), topk_weights.data_ptr(), w_gate_up.data_ptr(),
+                                 scale_gate_up.data_ptr(), w_down.data_ptr(), scale_down.data_ptr(),
+                                 out.data_ptr(), _dtype_code(out), _addr(workspace),
+                                 0 if workspace is None else workspace.numel() * workspace.element_size(), on.ptr),
+               "qk_w8a8_moe_layer")
+    return out
 
 
 def linear(x, w_q, sw, group_k: int = 0, output_scale: float = 1.0, out_dtype=None, stream=None):
