@@ -181,8 +181,8 @@ QK_API qk_status qk_silu_mul_quant_per_token_fp8(int m, int k, const void* gate,
  *     a     = max |t|;   rstd = 1 / sqrt(mean(r^2) + eps)
  *     z     = a * rstd;  scale = max(z, 1e-12f) / qmax     (qmax 127, or 448)
  *             fp8 with scale_ub: scale = min(scale, *scale_ub)
- *     inv   = qmax / a;  rstd / scale when the floor 1e-12 or the bound is
- *             what made the scale
+ *     inv   = qmax * (1 / a);  rstd / scale when the floor 1e-12 or the bound
+ *             is what made the scale
  *     q     = round_half_even(t * inv)               (int8)
  *             e4m3(clamp(t * inv, -448, 448))        (fp8)
  *     norm_out = t * rstd, rounded to x_dtype

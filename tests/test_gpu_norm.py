@@ -2,14 +2,15 @@
 
 Against the definition, in numpy:
 * residual_out, and the codes where the scale is neither floored nor bounded, bit for bit (they depend on
-  no sum): t = r * w, a = max |t|, inv = qmax / a, each one binary32 operation;
+  no sum): t = r * w, a = max |t|, inv = qmax * (1 / a), each step one binary32
+  operation;
 * everything against the formula in 64 bits.  With u = 2^-24 (half a binary32 step):
   - the squares are added by 256 or more threads, so a sum of k of them passes at most k/256 + 16
     additions: relative error of the sum (k/256 + 16) u, halved by the square root, then the mean, eps,
     square root and reciprocal: rstd within ((k/256 + 16)/2 + 4) u;
   - scale: + 3 u (a's own rounding, z, the division); norm_out in binary32: + 2 u (t, the product);
     in bf16 half a step, 2^-8, more;
-  - a code differs from qmax * t / a by at most half a unit (int8) plus four roundings of at most
+  - a code differs from qmax * t / a by at most half a unit (int8) plus five roundings of at most
     127 u; e4m3: half a step, 2^-4 relative (2^-10 among the subnormals)."""
 import numpy as np
 import pytest
@@ -69,7 +70,7 @@ def check(O, x, res, w, eps, got, fp8=False, ub=None):
     free = (whole == want) & (a64 * rstd > 1.001e-12)
     codes = host(q)
     with np.errstate(all="ignore"):
-        inv = np.float32(qmax) / np.abs(t).max(1)
+        inv = np.float32(qmax) * (np.float32(1) / np.abs(t).max(1))
         v32 = t * inv[:, None]
     if fp8:
         assert_bits(codes[free], O.f32_to_e4m3(np.clip(v32[free], -448, 448).astype(np.float32)), "codes")
@@ -80,7 +81,7 @@ def check(O, x, res, w, eps, got, fp8=False, ub=None):
         assert_bits(codes[free], np.rint(v32[free]).astype(np.int8), "codes")
         v = t64 * rstd[:, None] / want[:, None]
         assert np.all(np.abs(codes - v) <= 0.5 + 127 * (2 * tol + 8 * U)), "codes against 64 bits"
-        assert np.all(np.abs(codes[free] - v[free]) <= 0.5 + 127 * 4 * U), "codes against 64 bits"
+        assert np.all(np.abs(codes[free] - v[free]) <= 0.5 + 127 * 5 * U), "codes against 64 bits"
         assert codes.min() >= -127
     if y is not None:
         want_y = t64 * rstd[:, None]

@@ -7,8 +7,8 @@
 //     a = max |t|                        (exact)
 //     rstd = 1 / sqrt(mean(r^2) + eps)
 //     scale = max(a * rstd, 1e-12) / qmax, bounded by *ub (fp8)
-//     q = round(t * inv),  inv = qmax / a  (rstd / scale when the scale was
-//                                           clamped or bounded)
+//     q = round(t * inv),  inv = qmax * (1 / a)  (rstd / scale when the scale
+//                                                 was clamped or bounded)
 //     y = t * rstd                       (optional, rounded to x's type)
 // The norm's factor rstd cancels between a value and its row's scale, so the
 // codes need only t and a, and the maximum and the sum of squares are reduced
@@ -85,7 +85,8 @@ __device__ __forceinline__ RowFactors row_factors(const Args& p, float amax, flo
   const float z = __fmul_rn(amax, f.rstd);
   const float whole = __fdiv_rn(fmaxf(z, 1e-12f), qmax);
   f.scale = p.ub != nullptr ? fminf(whole, __ldg(p.ub)) : whole;
-  f.inv = (z >= 1e-12f && f.scale == whole) ? __fdiv_rn(qmax, amax) : __fdiv_rn(f.rstd, f.scale);
+  f.inv = (z >= 1e-12f && f.scale == whole) ? __fmul_rn(qmax, __fdiv_rn(1.0f, amax))
+                                                : __fdiv_rn(f.rstd, f.scale);
   return f;
 }
 

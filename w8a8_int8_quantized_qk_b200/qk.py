@@ -562,106 +562,95 @@ def w8a8_linear_fused(x, w_q, sw, output_scale: float = 1.0, out_dtype=None, wan
     return out, sa
 
 
-# The helpers below allocate on the stream they launch on (so a workspace that
-# is dropped on return is not handed out before the kernels have run) and on
-# the tensors' own device.
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+# The operators around the linear layer.  Their helpers allocate on the stream
+# they launch on (a workspace dropped on return is then not handed out before
+# the kernels have run) and on the tensors' own device, and check every tensor.
+# The checks and the call are the host's share of a decode step, where the
+# kernels take a few microseconds: they use the cheapest queries (get_device,
+# the raw stream) and build messages only for what they refuse.
+def _refuse(t, dev, dtype, shape, what):
+    if t.get_device() < 0:
+        _need_cuda(t)
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on device {t.get_device()}, others on {dev}")
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{what}: must be contiguous")
 
 
-def _same_device(x, *ts) -> None:
-    _need_cuda(x, *ts)
-    for t in ts:
-        if t is not None and t.device != x.device:
-            raise ValueError(f"tensors on {x.device} and {t.device}: one device is needed")
+def _dense(t, dev, dtype, shape, what) -> int:
+    """The address of a dense tensor of this device, type and shape."""
+    if t.get_device() != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(t, dev, dtype, shape, what)
+    return t.data_ptr()
 
 
-class _On:
-    """Makes `device` current, and `stream` (a torch stream, or None for the
-    current one) the stream that torch allocates for; .ptr is its handle."""
-
-    __slots__ = ("ctx", "ptr")
-
-    def __init__(self, device, stream):
-        torch = _torch()
-        self.ctx = None
-        if stream is not None:
-            _need(stream.device == device, f"stream of {stream.device}, tensors on {device}")
-            self.ctx = torch.cuda.stream(stream)
-        elif device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        self.ptr = _torch().cuda.current_stream().cuda_stream
-        return self
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _rows(t, dev, dtype, shape, what) -> int:
+    """Row stride, in elements, of a matrix whose rows are dense (a single row's own length)."""
+    if t.get_device() != dev or t.dtype != dtype or t.shape != shape or (t.stride(1) != 1 and shape[1] != 1):
+        _refuse(t, dev, dtype, shape, what)
+    return t.stride(0) if shape[0] > 1 else shape[1]
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
+def _on(dev: int, stream):
+    """None where `dev` is current and no other stream is asked for, else a context that makes it so."""
+    torch = _torch()
+    if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError(f"stream of device {stream.device.index}, tensors on {dev}")
+        return torch.cuda.stream(stream)
+    return torch.cuda.device(dev) if torch.cuda.current_device() != dev else None
 
 
-def _matrix(t, shape, dtype, what, dense=True):
-    """Checks a tensor's type, shape and layout (dense, or rows of any stride)."""
-    _need(t.dtype == dtype, f"{what}: expected {dtype}, got {t.dtype}")
-    _need(tuple(t.shape) == shape, f"{what}: expected shape {shape}, got {tuple(t.shape)}")
-    if dense:
-        _need(t.is_contiguous(), f"{what}: must be contiguous")
-    else:
-        _need(t.stride(-1) == 1 or shape[-1] == 1, f"{what}: the last dimension must be contiguous")
-
-
-def _row_stride(t) -> int:
-    """Row stride of a matrix in elements (a single row's own length)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _raw_stream(dev: int) -> int:
+    return _torch()._C._cuda_getCurrentRawStream(dev)
 
 
 def _rmsnorm_quant(x, weight, residual, eps, scale_ub, want_norm, residual_out, norm_out, q, scale, stream, fp8):
+    dev = x.get_device()
+    if dev < 0:
+        _need_cuda(x)
+    on = _on(dev, stream)
+    if on is not None:
+        with on:
+            return _rmsnorm_quant(x, weight, residual, eps, scale_ub, want_norm, residual_out, norm_out, q, scale,
+                                  None, fp8)
     torch = _torch()
-    _same_device(x, weight, residual, scale_ub, residual_out, norm_out, q, scale)
-    _need(x.dim() == 2, f"x: expected [m, k], got {tuple(x.shape)}")
-    m, k = shape = tuple(x.shape)
-    dt, code = x.dtype, _dtype_code(x)
-    codes = torch.uint8 if fp8 else torch.int8
-    _matrix(x, shape, dt, "x", dense=False)
-    _matrix(weight, (k,), dt, "weight")
-    _need(residual is not None or residual_out is None, "residual_out: needs a residual")
+    shape, dt = x.shape, x.dtype
+    code = _dtype_code(x)
+    if len(shape) != 2:
+        raise ValueError(f"x: expected [m, k], got {tuple(shape)}")
+    m, k = shape
+    ld_x = _rows(x, dev, dt, shape, "x")
+    ld_res = ld_out = 0
     if residual is not None:
-        _matrix(residual, shape, dt, "residual", dense=False)
-    if scale_ub is not None:
-        _matrix(scale_ub, (1,), torch.float32, "scale_ub")
-    with _On(x.device, stream) as on:
-        if residual_out is not None:
-            _matrix(residual_out, shape, dt, "residual_out", dense=False)
-        elif residual is not None:
-            residual_out = torch.empty(shape, dtype=dt, device=x.device)
-        if norm_out is not None:
-            _matrix(norm_out, shape, dt, "norm_out")
-        elif want_norm:
-            norm_out = torch.empty(shape, dtype=dt, device=x.device)
-        if q is None:
-            q = torch.empty(shape, dtype=codes, device=x.device)
+        ld_res = _rows(residual, dev, dt, shape, "residual")
+        if residual_out is None:
+            residual_out, ld_out = torch.empty(shape, dtype=dt, device=x.device), k
         else:
-            _matrix(q, shape, codes, "q")
-        if scale is None:
-            scale = torch.empty((m,), dtype=torch.float32, device=x.device)
-        else:
-            _matrix(scale, (m,), torch.float32, "scale")
-        head = (m, k, x.data_ptr(), _row_stride(x), _addr(residual), _row_stride(residual) if residual is not None
-                else 0, code, weight.data_ptr(), float(eps), _addr(residual_out),
-                _row_stride(residual_out) if residual_out is not None else 0, _addr(norm_out))
-        if fp8:
-            _check(qk_add_rmsnorm_quant_per_token_fp8(*head, _addr(scale_ub), q.data_ptr(), scale.data_ptr(), on.ptr),
-                   "qk_add_rmsnorm_quant_per_token_fp8")
-        else:
-            _check(qk_add_rmsnorm_quant_per_token(*head, q.data_ptr(), scale.data_ptr(), on.ptr),
-                   "qk_add_rmsnorm_quant_per_token")
+            ld_out = _rows(residual_out, dev, dt, shape, "residual_out")
+    elif residual_out is not None:
+        raise ValueError("residual_out: needs a residual")
+    if norm_out is not None:
+        _dense(norm_out, dev, dt, shape, "norm_out")
+    elif want_norm:
+        norm_out = torch.empty(shape, dtype=dt, device=x.device)
+    codes = torch.uint8 if fp8 else torch.int8
+    q = torch.empty(shape, dtype=codes, device=x.device) if q is None else q
+    scale = torch.empty((m,), dtype=torch.float32, device=x.device) if scale is None else scale
+    args = [m, k, x.data_ptr(), ld_x, None if residual is None else residual.data_ptr(), ld_res, code,
+            _dense(weight, dev, dt, (k,), "weight"), eps,
+            None if residual_out is None else residual_out.data_ptr(), ld_out,
+            None if norm_out is None else norm_out.data_ptr()]
+    if fp8:
+        args.append(None if scale_ub is None else _dense(scale_ub, dev, torch.float32, (1,), "scale_ub"))
+    args += (_dense(q, dev, codes, shape, "q"), _dense(scale, dev, torch.float32, (m,), "scale"), _raw_stream(dev))
+    L = lib()
+    st = (L.qk_add_rmsnorm_quant_per_token_fp8 if fp8 else L.qk_add_rmsnorm_quant_per_token)(*args)
+    if st != QK_OK:
+        raise QKError(st, "qk_add_rmsnorm_quant_per_token" + ("_fp8" if fp8 else ""))
     return q, scale, residual_out, norm_out
 
 
@@ -683,43 +672,55 @@ def add_rmsnorm_quant_per_token_fp8(x, weight, residual=None, eps: float = 1e-6,
                           True)
 
 
+def _workspace(workspace, need: int, dev: int, device):
+    """(address, bytes) of the caller's workspace, or of a new one of `need` bytes, and the new one."""
+    if workspace is None:
+        if not need:
+            return None, 0, None
+        workspace = _torch().empty((need,), dtype=_torch().uint8, device=device)
+        return workspace.data_ptr(), need, workspace
+    if workspace.get_device() != dev:
+        _refuse(workspace, dev, workspace.dtype, workspace.shape, "workspace")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
 def w8a8_lora_gemm(a, b, scale_a, scale_b, x, lora_a, lora_b, adapter_ids, lora_scale=None,
                    output_scale: float = 1.0, out_dtype=None, out=None, workspace=None, stream=None):
     """a int8 [m, k], b int8 [n, k], x [m, k] bf16/fp32 (the tokens before quantisation),
     lora_a bf16 [adapters, rank, k], lora_b bf16 [adapters, n, rank], adapter_ids int32 [m]
     (-1: none), lora_scale fp32 [adapters] or None -> out [m, n]."""
+    dev = a.get_device()
+    if dev < 0:
+        _need_cuda(a)
+    on = _on(dev, stream)
+    if on is not None:
+        with on:
+            return w8a8_lora_gemm(a, b, scale_a, scale_b, x, lora_a, lora_b, adapter_ids, lora_scale, output_scale,
+                                  out_dtype, out, workspace)
     torch = _torch()
-    _same_device(a, b, scale_a, scale_b, x, lora_a, lora_b, adapter_ids, lora_scale, out, workspace)
-    _need(a.dim() == 2 and b.dim() == 2, "a and b: expected [m, k] and [n, k]")
-    _need(lora_a.dim() == 3, "lora_a: expected [adapters, rank, k]")
+    if a.dim() != 2 or b.dim() != 2 or lora_a.dim() != 3:
+        raise ValueError("expected a [m, k], b [n, k] and lora_a [adapters, rank, k]")
     m, k = a.shape
     n = b.shape[0]
-    adapters, rank = lora_a.shape[:2]
-    _matrix(a, (m, k), torch.int8, "a")
-    _matrix(b, (n, k), torch.int8, "b")
-    _matrix(scale_a, (m,), torch.float32, "scale_a")
-    _matrix(scale_b, (n,), torch.float32, "scale_b")
-    _matrix(x, (m, k), x.dtype, "x")
-    _matrix(lora_a, (adapters, rank, k), torch.bfloat16, "lora_a")
-    _matrix(lora_b, (adapters, n, rank), torch.bfloat16, "lora_b")
-    _matrix(adapter_ids, (m,), torch.int32, "adapter_ids")
-    if lora_scale is not None:
-        _matrix(lora_scale, (adapters,), torch.float32, "lora_scale")
+    adapters, rank, _ = lora_a.shape
+    i8, f32, bf16 = torch.int8, torch.float32, torch.bfloat16
     x_code = _dtype_code(x)
-    with _On(a.device, stream) as on:
-        if out is None:
-            out = torch.empty((m, n), dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=a.device)
-        else:
-            _matrix(out, (m, n), out.dtype if out_dtype is None else out_dtype, "out")
-        need = qk_w8a8_lora_gemm_workspace_size(m, n, k, rank)
-        if need and workspace is None:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=a.device)
-        _check(qk_w8a8_lora_gemm(m, n, k, a.data_ptr(), b.data_ptr(), scale_a.data_ptr(), scale_b.data_ptr(),
-                                 float(output_scale), x.data_ptr(), x_code, adapters, rank, lora_a.data_ptr(),
-                                 lora_b.data_ptr(), _addr(lora_scale), adapter_ids.data_ptr(), out.data_ptr(),
-                                 _dtype_code(out), _addr(workspace),
-                                 0 if workspace is None else workspace.numel() * workspace.element_size(), on.ptr),
-               "qk_w8a8_lora_gemm")
+    if out is None:
+        out = torch.empty((m, n), dtype=bf16 if out_dtype is None else out_dtype, device=a.device)
+    L = lib()
+    ws, ws_bytes, hold = _workspace(workspace, L.qk_w8a8_lora_gemm_workspace_size(m, n, k, rank), dev, a.device)
+    st = L.qk_w8a8_lora_gemm(
+        m, n, k, _dense(a, dev, i8, (m, k), "a"), _dense(b, dev, i8, (n, k), "b"),
+        _dense(scale_a, dev, f32, (m,), "scale_a"), _dense(scale_b, dev, f32, (n,), "scale_b"), output_scale,
+        _dense(x, dev, x.dtype, (m, k), "x"), x_code, adapters, rank,
+        _dense(lora_a, dev, bf16, (adapters, rank, k), "lora_a"),
+        _dense(lora_b, dev, bf16, (adapters, n, rank), "lora_b"),
+        None if lora_scale is None else _dense(lora_scale, dev, f32, (adapters,), "lora_scale"),
+        _dense(adapter_ids, dev, torch.int32, (m,), "adapter_ids"),
+        _dense(out, dev, out.dtype if out_dtype is None else out_dtype, (m, n), "out"), _dtype_code(out),
+        ws, ws_bytes, _raw_stream(dev))
+    if st != QK_OK:
+        raise QKError(st, "qk_w8a8_lora_gemm")
     return out
 
 
@@ -728,36 +729,38 @@ def w8a8_moe_layer(a, scale_a, topk_ids, topk_weights, w_gate_up, scale_gate_up,
     """a int8 [m, hidden] (m <= 64), topk_ids int32 and topk_weights fp32 [m, topk],
     w_gate_up int8 [experts, 2 inter, hidden], w_down int8 [experts, hidden, inter] and their
     per-channel scales -> out [m, hidden]."""
+    dev = a.get_device()
+    if dev < 0:
+        _need_cuda(a)
+    on = _on(dev, stream)
+    if on is not None:
+        with on:
+            return w8a8_moe_layer(a, scale_a, topk_ids, topk_weights, w_gate_up, scale_gate_up, w_down, scale_down,
+                                  out_dtype, out, workspace)
     torch = _torch()
-    _same_device(a, scale_a, topk_ids, topk_weights, w_gate_up, scale_gate_up, w_down, scale_down, out, workspace)
-    _need(a.dim() == 2 and topk_ids.dim() == 2, "a and topk_ids: expected [m, hidden] and [m, topk]")
-    _need(w_down.dim() == 3, "w_down: expected [experts, hidden, inter]")
+    if a.dim() != 2 or topk_ids.dim() != 2 or w_down.dim() != 3:
+        raise ValueError("expected a [m, hidden], topk_ids [m, topk] and w_down [experts, hidden, inter]")
     m, hidden = a.shape
     topk = topk_ids.shape[1]
     experts, _, inter = w_down.shape
-    _matrix(a, (m, hidden), torch.int8, "a")
-    _matrix(scale_a, (m,), torch.float32, "scale_a")
-    _matrix(topk_ids, (m, topk), torch.int32, "topk_ids")
-    _matrix(topk_weights, (m, topk), torch.float32, "topk_weights")
-    _matrix(w_gate_up, (experts, 2 * inter, hidden), torch.int8, "w_gate_up")
-    _matrix(scale_gate_up, (experts, 2 * inter), torch.float32, "scale_gate_up")
-    _matrix(w_down, (experts, hidden, inter), torch.int8, "w_down")
-    _matrix(scale_down, (experts, hidden), torch.float32, "scale_down")
-    with _On(a.device, stream) as on:
-        if out is None:
-            out = torch.empty((m, hidden), dtype=torch.bfloat16 if out_dtype is None else out_dtype,
-                              device=a.device)
-        else:
-            _matrix(out, (m, hidden), out.dtype if out_dtype is None else out_dtype, "out")
-        need = qk_w8a8_moe_layer_workspace_size(m, hidden, inter, topk)
-        if need and workspace is None:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=a.device)
-        _check(qk_w8a8_moe_layer(m, hidden, inter, experts, topk, a.data_ptr(), scale_a.data_ptr(),
-                                 topk_ids.data_ptr(), topk_weights.data_ptr(), w_gate_up.data_ptr(),
-                                 scale_gate_up.data_ptr(), w_down.data_ptr(), scale_down.data_ptr(),
-                                 out.data_ptr(), _dtype_code(out), _addr(workspace),
-                                 0 if workspace is None else workspace.numel() * workspace.element_size(), on.ptr),
-               "qk_w8a8_moe_layer")
+    i8, f32 = torch.int8, torch.float32
+    if out is None:
+        out = torch.empty((m, hidden), dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=a.device)
+    L = lib()
+    ws, ws_bytes, hold = _workspace(workspace, L.qk_w8a8_moe_layer_workspace_size(m, hidden, inter, topk), dev,
+                                    a.device)
+    st = L.qk_w8a8_moe_layer(
+        m, hidden, inter, experts, topk, _dense(a, dev, i8, (m, hidden), "a"),
+        _dense(scale_a, dev, f32, (m,), "scale_a"), _dense(topk_ids, dev, torch.int32, (m, topk), "topk_ids"),
+        _dense(topk_weights, dev, f32, (m, topk), "topk_weights"),
+        _dense(w_gate_up, dev, i8, (experts, 2 * inter, hidden), "w_gate_up"),
+        _dense(scale_gate_up, dev, f32, (experts, 2 * inter), "scale_gate_up"),
+        _dense(w_down, dev, i8, (experts, hidden, inter), "w_down"),
+        _dense(scale_down, dev, f32, (experts, hidden), "scale_down"),
+        _dense(out, dev, out.dtype if out_dtype is None else out_dtype, (m, hidden), "out"), _dtype_code(out),
+        ws, ws_bytes, _raw_stream(dev))
+    if st != QK_OK:
+        raise QKError(st, "qk_w8a8_moe_layer")
     return out
 
 
