@@ -442,7 +442,8 @@ QK_API size_t qk_w8a8_lora_gemm_workspace_size(int m, int n, int k, int rank);
  *
  * m              tokens, 0 .. 64 (0: no-op; more: QK_ERR_UNSUPPORTED)
  * hidden, inter  > 0, multiples of 16, <= 133144 (QK_ERR_OVERFLOW_BOUND)
- * num_experts    1 .. 1024;  topk  1 .. 32 (more: QK_ERR_UNSUPPORTED)
+ * num_experts    1 .. 1024;  topk  1 .. 32 (more: QK_ERR_UNSUPPORTED);
+ *                num_experts * 2 * inter and num_experts * hidden below 2^31
  * a, scale_a     [m, hidden] int8, 16-B aligned, and [m] fp32
  * topk_ids, topk_weights   [m, topk] int32 and fp32, 4-B aligned
  * w_gate_up      [num_experts, 2 * inter, hidden] int8: an expert's gate rows,
@@ -463,8 +464,10 @@ QK_API qk_status qk_w8a8_moe_layer(int m, int hidden, int inter, int num_experts
                                    const float* scale_down, void* out, qk_dtype out_dtype,
                                    void* workspace, size_t workspace_bytes, qk_stream stream);
 
-/* Bytes of workspace qk_w8a8_moe_layer needs (0 for sizes it would reject). */
-QK_API size_t qk_w8a8_moe_layer_workspace_size(int m, int hidden, int inter, int topk);
+/* Bytes of workspace qk_w8a8_moe_layer needs on the current device (0 for
+ * sizes it would reject, and without a usable device). */
+QK_API size_t qk_w8a8_moe_layer_workspace_size(int m, int hidden, int inter, int num_experts,
+                                               int topk);
 
 /*
  * qk_quantize_static -- static per-tensor INT8 ("write-int8-quantized-

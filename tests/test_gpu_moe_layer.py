@@ -146,7 +146,7 @@ def test_moe_layer_workspace(m):
     need_gpu()
     p = make(m, 4, 2, 512, 272, seed=m)
     first = call(p)
-    need = qk.qk_w8a8_moe_layer_workspace_size(m, 512, 272, 2)
+    need = qk.qk_w8a8_moe_layer_workspace_size(m, 512, 272, 4, 2)
     for fill in (0, 255, 127):
         ws = torch.full((need + 64,), fill, dtype=torch.uint8, device="cuda")
         buf = torch.full((m + 2, 512), 3.0, dtype=torch.bfloat16, device="cuda")

@@ -132,6 +132,7 @@ def _moe(m=4, h=32, i=48, e=3, topk=2, a=P16, sa=P16, ids=P16, wt=P16, w13=P16, 
     (dict(m=65), qk.QK_ERR_UNSUPPORTED),
     (dict(topk=33), qk.QK_ERR_UNSUPPORTED),
     (dict(e=1025), qk.QK_ERR_UNSUPPORTED),
+    (dict(e=1024, i=1 << 20), qk.QK_ERR_OVERFLOW_BOUND),
     (dict(a=NULL), qk.QK_ERR_INVALID_ARG),
     (dict(sa=NULL), qk.QK_ERR_INVALID_ARG),
     (dict(ids=NULL), qk.QK_ERR_INVALID_ARG),
@@ -161,9 +162,9 @@ def test_workspace_queries():
                 (4, 16, 133152, 8)):
         assert qk.qk_w8a8_lora_gemm_workspace_size(*bad) == 0
     assert qk.qk_w8a8_lora_gemm_workspace_size(4, 16, 32, 8) >= 4 * 8 * 4
-    for bad in ((0, 32, 48, 2), (65, 32, 48, 2), (4, 40, 48, 2), (4, 32, 24, 2), (4, 32, 48, 0), (4, 32, 48, 33)):
+    for bad in ((0, 32, 48, 3, 2), (65, 32, 48, 3, 2), (4, 40, 48, 3, 2), (4, 32, 24, 3, 2), (4, 32, 48, 0, 2),
+                (4, 32, 48, 3, 0), (4, 32, 48, 3, 33), (4, 32, 48, 1025, 2)):
         assert qk.qk_w8a8_moe_layer_workspace_size(*bad) == 0
-    assert qk.qk_w8a8_moe_layer_workspace_size(4, 32, 48, 2) >= 8 * 48
 
 
 def test_helpers_refuse_host_tensors():

@@ -745,37 +745,46 @@ qk_status qk_w8a8_lora_gemm(int m, int n, int k, const int8_t* a, const int8_t* 
   return cuda_status(lora::launch_expand(la, dev->sms, s), "adapter expand launch");
 }
 
-// ---- a MoE layer for a few tokens; the workspace holds h, y, the scales of
-// h and its int8 values
+// ---- a MoE layer for a few tokens; the workspace holds the routing, the gate
+// and up sums, the down sums, the scales of h and its int8 values
 namespace {
-constexpr int kMoeLayerTokens = 64, kMoeLayerTopk = 32, kMoeLayerExperts = 1024;
+constexpr int kMoeLayerTokens = 64, kMoeLayerTopk = 32, kMoeLayerExperts = moe::kMaxExperts;
 
 struct MoeLayout {
-  size_t h, y, sh, q, total;  // byte offsets
+  size_t gu, part, sh, q, total;  // byte offsets (the routing is at 0)
 };
 
-MoeLayout moe_layout(int m, int hidden, int inter, int topk) {
+MoeLayout moe_layout(int m, int hidden, int inter, int topk, const stream::Plan& up, const stream::Plan& down) {
   const size_t pairs = static_cast<size_t>(m) * topk;
   MoeLayout l;
-  l.h = 0;
-  l.y = l.h + round256(pairs * inter * 4);
-  l.sh = l.y + round256(pairs * hidden * 4);
+  l.gu = round256(sizeof(moe::Routing));
+  l.part = l.gu + round256(pairs * inter * 8 * up.ksplit);
+  l.sh = l.part + round256(pairs * hidden * 4 * down.ksplit);
   l.q = l.sh + round256(pairs * 4);
   l.total = l.q + round256(pairs * inter);
   return l;
 }
 
-qk_status moe_layer_check(int m, int hidden, int inter, int topk) {
-  if (m < 0 || hidden <= 0 || inter <= 0 || (hidden % 16) != 0 || (inter % 16) != 0 || topk < 1)
+qk_status moe_layer_check(int m, int hidden, int inter, int num_experts, int topk) {
+  if (m < 0 || hidden <= 0 || inter <= 0 || (hidden % 16) != 0 || (inter % 16) != 0 || topk < 1 ||
+      num_experts < 1)
     return QK_ERR_INVALID_ARG;
   if (hidden > kMaxK || inter > kMaxK) return QK_ERR_OVERFLOW_BOUND;
-  return (m > kMoeLayerTokens || topk > kMoeLayerTopk) ? QK_ERR_UNSUPPORTED : QK_OK;
+  if (static_cast<int64_t>(num_experts) * 2 * inter > INT32_MAX ||
+      static_cast<int64_t>(num_experts) * hidden > INT32_MAX)
+    return QK_ERR_INVALID_ARG;
+  if (m > kMoeLayerTokens || topk > kMoeLayerTopk || num_experts > kMoeLayerExperts) return QK_ERR_UNSUPPORTED;
+  return QK_OK;
 }
 }  // namespace
 
-size_t qk_w8a8_moe_layer_workspace_size(int m, int hidden, int inter, int topk) {
-  if (moe_layer_check(m, hidden, inter, topk) != QK_OK || m == 0) return 0;
-  return moe_layout(m, hidden, inter, topk).total;
+size_t qk_w8a8_moe_layer_workspace_size(int m, int hidden, int inter, int num_experts, int topk) {
+  const DeviceInfo* dev = nullptr;
+  if (moe_layer_check(m, hidden, inter, num_experts, topk) != QK_OK || m == 0 || check_device(&dev) != QK_OK)
+    return 0;
+  stream::Plan up, down;
+  moe::plans(m, hidden, inter, num_experts, topk, dev->sms, &up, &down);
+  return moe_layout(m, hidden, inter, topk, up, down).total;
 }
 
 qk_status qk_w8a8_moe_layer(int m, int hidden, int inter, int num_experts, int topk, const int8_t* a,
@@ -783,10 +792,8 @@ qk_status qk_w8a8_moe_layer(int m, int hidden, int inter, int num_experts, int t
                             const int8_t* w_gate_up, const float* scale_gate_up, const int8_t* w_down,
                             const float* scale_down, void* out, qk_dtype out_dtype, void* workspace,
                             size_t workspace_bytes, qk_stream stream) {
-  qk_status st = moe_layer_check(m, hidden, inter, topk);
+  qk_status st = moe_layer_check(m, hidden, inter, num_experts, topk);
   if (st != QK_OK) return st;
-  if (num_experts < 1) return QK_ERR_INVALID_ARG;
-  if (num_experts > kMoeLayerExperts) return QK_ERR_UNSUPPORTED;
   if (out_dtype != QK_F32 && out_dtype != QK_BF16) return QK_ERR_INVALID_ARG;
   if (m == 0) return QK_OK;
   if (a == nullptr || scale_a == nullptr || topk_ids == nullptr || topk_weights == nullptr ||
@@ -800,30 +807,35 @@ qk_status qk_w8a8_moe_layer(int m, int hidden, int inter, int num_experts, int t
   const DeviceInfo* dev = nullptr;
   st = check_device(&dev);
   if (st != QK_OK) return st;
-  const MoeLayout l = moe_layout(m, hidden, inter, topk);
+  moe::Args g = {};
+  moe::plans(m, hidden, inter, num_experts, topk, dev->sms, &g.up, &g.down);
+  const MoeLayout l = moe_layout(m, hidden, inter, topk, g.up, g.down);
   if (workspace == nullptr || workspace_bytes < l.total || !aligned(workspace, 256)) return QK_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
-  moe::Args g = {};
   g.m = m;
   g.hidden = hidden;
   g.inter = inter;
   g.experts = num_experts;
   g.topk = topk;
-  g.a = a;
+  g.topk_inv = (65536 + topk - 1) / topk;
   g.sa = scale_a;
   g.ids = topk_ids;
   g.wt = topk_weights;
-  g.w13 = w_gate_up;
   g.s13 = scale_gate_up;
-  g.w2 = w_down;
   g.s2 = scale_down;
-  g.h = reinterpret_cast<float*>(ws + l.h);
-  g.y = reinterpret_cast<float*>(ws + l.y);
+  g.routing = reinterpret_cast<moe::Routing*>(ws);
+  g.gu = reinterpret_cast<int32_t*>(ws + l.gu);
+  g.part = reinterpret_cast<int32_t*>(ws + l.part);
   g.sh = reinterpret_cast<float*>(ws + l.sh);
   g.q = reinterpret_cast<int8_t*>(ws + l.q);
   g.out = out;
   g.out_bf16 = out_dtype == QK_BF16;
-  return cuda_status(moe::launch(g, dev->sms, reinterpret_cast<cudaStream_t>(stream)), "moe layer launch");
+  int dev_id = 0;
+  cudaGetDevice(&dev_id);
+  cudaError_t e = cudaSuccess;
+  const int r = moe::launch(g, a, w_gate_up, w_down, dev_id, dev->sms, reinterpret_cast<cudaStream_t>(stream), &e);
+  if (r == 1) return cuda_status(cudaErrorInvalidValue, "tensor map encoding");
+  return r == 0 ? QK_OK : cuda_status(e, "moe layer launch");
 }
 
 qk_status qk_w8a8_linear(int m, int n, int k, const void* x, qk_dtype x_dtype, const int8_t* b,

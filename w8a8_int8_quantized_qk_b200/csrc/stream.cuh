@@ -1,0 +1,265 @@
+// stream.cuh -- int8 weights streamed past at most 64 int8 tokens on the
+// tensor core: the core of the MoE layer for a few tokens and of the
+// projection with adapters for small batches.
+//
+// The products are bound by reading the weights once, so the weight rows take
+// the M side of the MMA (128 rows) and the tokens its N side (16 .. 64), and
+// 128-row tiles of 128 K bytes flow through a ring that holds about 200 KB on
+// every SM: the loads need no registers and no thread waits for them.  The
+// warp matrix instruction (mma.m16n8k32, fed from registers) was built first;
+// it takes 32 cycles a warp for 512 weight bytes on this part, which is 47 %
+// of the pipe at full HBM rate for 8 tokens and the bound beyond 16, and its
+// chains of dependent products kept 8 tokens of 2 experts at 4.9 TB/s.
+//
+// The sums leave as int32, one slice for each K range a unit is cut into (so
+// that few row blocks still occupy every SM); what reads them adds the slices,
+// exactly.
+#pragma once
+
+#include "gemm_sm100.cuh"
+#include "qk_common.cuh"
+
+namespace qk {
+namespace stream {
+
+constexpr int kThreads = 192;      // producer warp, MMA warp, 4 epilogue warps
+constexpr int kRows = 128;         // weight rows of a unit
+constexpr int kK = 128;            // K bytes of a stage
+constexpr int kMaxStages = 12;
+constexpr int kMaxTokens = 64;     // N side of one unit
+constexpr int kTmemCols = 128;     // two accumulators of 64 columns
+constexpr size_t kRingBytes = 212 * 1024;
+
+struct Plan {
+  int nb;        // tokens of a unit: 16, 32, 48 or 64
+  int stages;
+  int num_kb;    // K blocks of a row
+  int ksplit;    // K ranges
+  int kbs;       // K blocks of a range (the last may have fewer)
+  int row_blocks;
+  int n;         // weight rows (per expert)
+};
+
+__host__ __device__ inline int stage_bytes(int nb) { return kRows * kK + nb * kK; }
+
+// `tokens`: N side wanted; `sets`: independent sets of n rows (experts).  K is
+// cut until there are about five units an SM, no range shorter than four
+// blocks: an uneven last round then costs a fifth of the time at most, and in
+// fact less, since an SM streams faster while others have ended.
+inline Plan plan(int tokens, int64_t sets, int n, int k, int num_sms) {
+  Plan p;
+  p.nb = tokens >= kMaxTokens ? kMaxTokens : (tokens + 15) / 16 * 16;
+  const int fit = static_cast<int>(kRingBytes / stage_bytes(p.nb));
+  p.stages = fit < kMaxStages ? fit : kMaxStages;
+  p.num_kb = (k + kK - 1) / kK;
+  p.row_blocks = (n + kRows - 1) / kRows;
+  p.n = n;
+  p.ksplit = 1;
+  while (p.ksplit < 8 && sets * p.row_blocks * p.ksplit < 5LL * num_sms && p.num_kb / (2 * p.ksplit) >= 4)
+    p.ksplit *= 2;
+  p.kbs = (p.num_kb + p.ksplit - 1) / p.ksplit;
+  p.ksplit = (p.num_kb + p.kbs - 1) / p.kbs;
+  return p;
+}
+
+inline size_t smem_bytes(const Plan& p) {
+  return 1024 + static_cast<size_t>(p.stages) * stage_bytes(p.nb);
+}
+
+struct Bars {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+// One unit: 128 weight rows, a K range and the tokens they meet.
+struct Span {
+  int w_row, x_row;  // first rows in the two tensor maps
+  int kb0, kb1;
+};
+
+__device__ __forceinline__ uint32_t tmem_ld_x1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
+  return r;
+}
+
+// The roles.  P has:
+//   static constexpr bool kEarlyWeights   the first weights are requested before
+//                                     the wait for the previous kernel (which must
+//                                     not write them)
+//   Walk start(); bool span(Walk&, int u, Span&)   unit u (a Walk goes upward
+//                                     only); false past the last
+//   void store(Walk&, int u, const Span&, uint32_t tmem, int row)   unit u's sums:
+//                                     row `row` of the unit, tokens in TMEM columns
+template <class P>
+__device__ __forceinline__ void run(const P& prob, const Plan& pl, Bars& s, uint8_t* ring, const CUtensorMap* tmW,
+                                    const CUtensorMap* tmX) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int stages = pl.stages, sb = stage_bytes(pl.nb);
+  const int bid = static_cast<int>(blockIdx.x), grid = static_cast<int>(gridDim.x);
+  const uint32_t ring0 = smem_addr(ring);
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0, pre = 0;
+      uint32_t phase = 0, issued = 0;
+      bool ok = true;
+      typename P::Walk w = prob.start();
+      Span u;
+      if constexpr (P::kEarlyWeights) {
+        typename P::Walk we = prob.start();
+        for (int unit = bid; pre < stages && prob.span(we, unit, u); unit += grid)
+          for (int kb = u.kb0; kb < u.kb1 && pre < stages; ++kb, ++pre) {
+            const uint32_t fb = smem_addr(&s.full[pre]);
+            mbar_arrive_expect_tx(fb, static_cast<uint32_t>(sb));
+            tma_load_2d(ring0 + pre * sb, tmW, fb, kb * kK, u.w_row);
+          }
+        griddep_wait();
+      }
+      for (int unit = bid; ok && prob.span(w, unit, u); unit += grid) {
+        for (int kb = u.kb0; kb < u.kb1; ++kb) {
+          const uint32_t fb = smem_addr(&s.full[stage]);
+          if (pre > 0) {
+            --pre;  // this stage's weights are on their way
+          } else {
+            if (!mbar_wait(smem_addr(&s.empty[stage]), phase ^ 1u, &s.abort)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(fb, static_cast<uint32_t>(sb));
+            tma_load_2d(ring0 + stage * sb, tmW, fb, kb * kK, u.w_row);
+          }
+          tma_load_2d(ring0 + stage * sb + kRows * kK, tmX, fb, kb * kK, u.x_row);
+          ++issued;
+          if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // No copy may still be landing in shared memory when the CTA exits: wait
+      // (bounded, ignoring the abort flag) for the last copies issued.
+      const uint32_t n = static_cast<uint32_t>(stages);
+      for (uint32_t i = issued > n ? issued - n : 0u; i < issued; ++i)
+        mbar_wait(smem_addr(&s.full[i % n]), (i / n) & 1u, nullptr);
+    }
+    __syncwarp();
+    if constexpr (P::kEarlyWeights) griddep_launch_dependents();
+  } else if (warp == 1) {
+    if constexpr (P::kEarlyWeights) {
+      griddep_wait();
+      griddep_launch_dependents();
+    }
+    if (lane == 0) {
+      const uint32_t idesc = idesc_i8(kRows, pl.nb);
+      int stage = 0;
+      uint32_t phase = 0, abuf = 0, aphase = 0;
+      bool ok = true;
+      typename P::Walk w = prob.start();
+      Span u;
+      for (int unit = bid; ok && prob.span(w, unit, u); unit += grid) {
+        if (!mbar_wait(smem_addr(&s.acc_empty[abuf]), aphase ^ 1u, &s.abort)) break;
+        tc_fence_after();
+        const uint32_t d = s.tmem_base + abuf * kMaxTokens;
+        for (int kb = u.kb0; kb < u.kb1; ++kb) {
+          if (!mbar_wait(smem_addr(&s.full[stage]), phase, &s.abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a0 = ring0 + stage * sb, b0 = a0 + kRows * kK;
+#pragma unroll
+          for (int kk = 0; kk < kK / gemm::UMMA_K; ++kk)
+            mma_i8(d, sdesc_k_sw128(a0 + kk * gemm::UMMA_K), sdesc_k_sw128(b0 + kk * gemm::UMMA_K), idesc,
+                   kb > u.kb0 || kk > 0);
+          mma_commit(smem_addr(&s.empty[stage]));
+          if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (ok) {
+          mma_commit(smem_addr(&s.acc_full[abuf]));
+          abuf ^= 1u;
+          if (abuf == 0) aphase ^= 1u;
+        }
+      }
+      // Every MMA issued must be complete before the TMEM can be released.
+      mma_commit(smem_addr(&s.drain));
+      mbar_wait(smem_addr(&s.drain), 0u, nullptr);
+    }
+    __syncwarp();
+  } else {
+    if constexpr (P::kEarlyWeights) {
+      griddep_wait();
+      griddep_launch_dependents();
+    }
+    const int quad = warp & 3;
+    uint32_t abuf = 0, aphase = 0;
+    typename P::Walk w = prob.start();
+    Span u;
+    for (int unit = bid; prob.span(w, unit, u); unit += grid) {
+      if (!gemm::warp_wait(smem_addr(&s.acc_full[abuf]), aphase, &s.abort)) break;
+      tc_fence_after();
+      prob.store(w, unit, u, s.tmem_base + abuf * kMaxTokens + (static_cast<uint32_t>(quad * 32) << 16),
+                 quad * 32 + lane);
+      tc_fence_before();
+      if (lane == 0) mbar_arrive(smem_addr(&s.acc_empty[abuf]));
+      abuf ^= 1u;
+      if (abuf == 0) aphase ^= 1u;
+    }
+  }
+}
+
+__device__ __forceinline__ void setup(Bars& s, const Plan& pl) {
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < pl.stages; ++i) {
+      mbar_init(smem_addr(&s.full[i]), 1);
+      mbar_init(smem_addr(&s.empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&s.acc_full[i]), 1);
+      mbar_init(smem_addr(&s.acc_empty[i]), 4);
+    }
+    mbar_init(smem_addr(&s.drain), 1);
+    s.abort = 0;
+    fence_mbar_init();
+  }
+  if ((threadIdx.x >> 5) == 1) {
+    tmem_alloc(smem_addr(&s.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+}
+
+__device__ __forceinline__ void teardown(Bars& s) {
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if ((threadIdx.x >> 5) == 1) tmem_dealloc(s.tmem_base, kTmemCols);
+}
+
+__device__ __forceinline__ uint8_t* ring_of(uint8_t* raw) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+}
+
+// Sums of columns [0, count) of one row of a unit: out(token, value).
+template <class F>
+__device__ __forceinline__ void each_column(uint32_t tmem, int count, F&& out) {
+  for (int c0 = 0; c0 < count; c0 += 16) {
+    uint32_t v[16];
+    __syncwarp();
+    tmem_ld_32x32b_x16(tmem + c0, v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+      if (c0 + c < count) out(c0 + c, static_cast<int>(v[c]));
+  }
+}
+
+}  // namespace stream
+}  // namespace qk

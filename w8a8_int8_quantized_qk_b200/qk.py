@@ -77,7 +77,7 @@ _SIGNATURES = {
                                          _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int, _P, ctypes.c_size_t,
                                          _P]),
     "qk_w8a8_moe_layer_workspace_size": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int, ctypes.c_int,
-                                                           ctypes.c_int]),
+                                                           ctypes.c_int, ctypes.c_int]),
     "qk_quantize_static": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _P, ctypes.c_int, _P, _P, _P]),
     "qk_weight_row_sums": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _P, _P, _P]),
     "qk_w8a8_gemm_asym": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, _P, _P, _P, _P, _P,
@@ -213,8 +213,8 @@ def qk_w8a8_moe_layer(m, hidden, inter, num_experts, topk, a, scale_a, topk_ids,
                                    workspace_bytes, stream)
 
 
-def qk_w8a8_moe_layer_workspace_size(m, hidden, inter, topk) -> int:
-    return lib().qk_w8a8_moe_layer_workspace_size(m, hidden, inter, topk)
+def qk_w8a8_moe_layer_workspace_size(m, hidden, inter, num_experts, topk) -> int:
+    return lib().qk_w8a8_moe_layer_workspace_size(m, hidden, inter, num_experts, topk)
 
 
 def qk_quantize_static(m, k, x, x_dtype, scale, q, stream) -> int:
@@ -747,8 +747,8 @@ def w8a8_moe_layer(a, scale_a, topk_ids, topk_weights, w_gate_up, scale_gate_up,
     if out is None:
         out = torch.empty((m, hidden), dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=a.device)
     L = lib()
-    ws, ws_bytes, hold = _workspace(workspace, L.qk_w8a8_moe_layer_workspace_size(m, hidden, inter, topk), dev,
-                                    a.device)
+    ws, ws_bytes, hold = _workspace(workspace, L.qk_w8a8_moe_layer_workspace_size(m, hidden, inter, experts, topk),
+                                    dev, a.device)
     st = L.qk_w8a8_moe_layer(
         m, hidden, inter, experts, topk, _dense(a, dev, i8, (m, hidden), "a"),
         _dense(scale_a, dev, f32, (m,), "scale_a"), _dense(topk_ids, dev, torch.int32, (m, topk), "topk_ids"),
