@@ -453,7 +453,7 @@ QK_API size_t qk_w8a8_lora_gemm_workspace_size(int m, int n, int k, int rank);
  * out            [m, hidden] out_dtype
  * workspace      qk_w8a8_moe_layer_workspace_size() bytes, 256-B aligned, with
  *                any contents; owned by the call as for qk_w8a8_lora_gemm
- * Alignment: 16 bytes for a, the weights and out, 4 for the scales.
+ * Alignment: 16 bytes for a, the weights, their scales and out, 4 for scale_a.
  * Errors: QK_ERR_INVALID_ARG, QK_ERR_MISALIGNED, QK_ERR_OVERFLOW_BOUND,
  *         QK_ERR_WORKSPACE, QK_ERR_UNSUPPORTED, QK_ERR_CUDA.
  */

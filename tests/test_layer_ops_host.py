@@ -149,8 +149,8 @@ def _moe(m=4, h=32, i=48, e=3, topk=2, a=P16, sa=P16, ids=P16, wt=P16, w13=P16, 
     (dict(sa=P2), qk.QK_ERR_MISALIGNED),
     (dict(ids=P2), qk.QK_ERR_MISALIGNED),
     (dict(wt=P2), qk.QK_ERR_MISALIGNED),
-    (dict(s13=P2), qk.QK_ERR_MISALIGNED),
-    (dict(s2=P2), qk.QK_ERR_MISALIGNED),
+    (dict(s13=P8), qk.QK_ERR_MISALIGNED),
+    (dict(s2=P8), qk.QK_ERR_MISALIGNED),
     (dict(m=0), qk.QK_OK),
 ])
 def test_moe_layer_rejects(kw, expect):

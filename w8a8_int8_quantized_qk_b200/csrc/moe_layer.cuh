@@ -18,8 +18,9 @@
 //      is gathered or copied;
 //   2. scales, silu, the row's maximum and its quantisation, one CTA or cluster
 //      per pair, into rows sorted by expert;
-//   3. the down rows past each expert's rows; its first 200 KB of weights an SM
-//      are requested while kernel 2 still runs;
+//   3. the down rows past each expert's rows; a CTA starts, sorts the pairs and
+//      requests its first 180 KB of weights as soon as one of kernel 1 has left
+//      its SM, while the others and kernel 2 still run;
 //   4. the weighted sum.
 #pragma once
 
@@ -49,7 +50,10 @@ struct Args {
   const float* wt;      // [m, topk]
   const float* s13;     // [experts, 2 inter]
   const float* s2;      // [experts, hidden]
-  Routing* routing;     // workspace, like the following
+  int4* by_pos;         // workspace, like the following; [pairs]: {pair, expert, first tile of gate and up, blocks of a CTA there}, pair -1 past
+                        // the last, in the sorted order
+  int4* by_pair;        // [pairs]: {expert or -1, first tile of the down product, tiles from one row block to the
+                        // next, blocks of a CTA there}
   int32_t* gu;          // [slices, pairs, 2 inter]: the gate and up sums
   int8_t* q;            // [pairs, inter], sorted by expert
   float* sh;            // [pairs]
@@ -57,6 +61,7 @@ struct Args {
   void* out;            // [m, hidden]
   int out_bf16;
   stream::Plan up, down;
+  int up_grid, down_grid;
 };
 
 __device__ __forceinline__ int expert_of(const Args& p, int pair) {
@@ -117,36 +122,27 @@ __device__ __forceinline__ void route(const Args& p, Routing& r, int* cnt) {
   __syncthreads();
 }
 
-// Units: expert by expert, a row block and K range at a time; an expert's token
-// tiles (down) innermost, so that weights read again come from L2.
-struct Walk {
-  int i, base;  // active expert i, whose first unit is `base`
-};
-
-// Gate and up: rows of w13 past all tokens.
+// Gate and up: rows of w13 past all tokens; tile t is row block t % row_blocks
+// of active expert t / row_blocks.
 struct GateUp {
   static constexpr bool kEarlyWeights = false;
-  using Walk = moe::Walk;
+  struct Walk {
+    int i;
+  };
   const Args& p;
   const Routing& r;
-  __device__ __forceinline__ Walk start() const { return {0, 0}; }
-  __device__ __forceinline__ bool span(Walk& w, int u, stream::Span& s) const {
-    const stream::Plan& pl = p.up;
-    const int per = pl.row_blocks * pl.ksplit;
-    w.i = u / per;
-    if (w.i >= r.active) return false;
-    const int j = u - w.i * per, rb = j / pl.ksplit, ks = j - rb * pl.ksplit;
-    s.w_row = r.act[w.i] * pl.n + rb * stream::kRows;
-    s.x_row = 0;
-    s.kb0 = ks * pl.kbs;
-    s.kb1 = min(pl.num_kb, s.kb0 + pl.kbs);
-    return true;
+  __device__ __forceinline__ int tiles() const { return r.active * p.up.row_blocks; }
+  __device__ __forceinline__ Walk start() const { return {0}; }
+  __device__ __forceinline__ stream::Tile tile(Walk& w, int t) const {
+    w.i = t / p.up.row_blocks;
+    return {r.act[w.i] * p.up.n + (t - w.i * p.up.row_blocks) * stream::kRows, 0};
   }
   // The columns of the expert's tokens, four at a time, to their pairs' rows.
-  __device__ __forceinline__ void store(const Walk& w, int, const stream::Span& s, uint32_t tmem, int row) const {
+  __device__ __forceinline__ void store(const Walk& w, int, int slice, const stream::Tile& s, uint32_t tmem,
+                                        int row) const {
     const stream::Plan& pl = p.up;
     const int col = s.w_row - r.act[w.i] * pl.n + row, lo = r.off[w.i], hi = r.off[w.i + 1];
-    int32_t* out = p.gu + static_cast<int64_t>(s.kb0 / pl.kbs) * (p.m * p.topk) * pl.n + col;
+    int32_t* out = p.gu + static_cast<int64_t>(slice) * (p.m * p.topk) * pl.n + col;
     for (int j = lo; j < hi; j += 4) {
       uint32_t v[4];
       __syncwarp();
@@ -161,43 +157,66 @@ struct GateUp {
   }
 };
 
-// Down: rows of w2 past an expert's rows of q, nb at a time.
+// Down: rows of w2 past an expert's rows of q, nb at a time: expert by expert, a
+// row block's token tiles innermost, so that weights read again come from L2.
+__device__ __forceinline__ int token_tiles(const Args& p, const Routing& r, int i) {
+  const int n = r.off[i + 1] - r.off[i];
+  return n <= p.down.nb ? 1 : (n + p.down.nb - 1) / p.down.nb;
+}
+__device__ __forceinline__ int down_tiles(const Args& p, const Routing& r) {
+  int t = 0;
+  for (int i = 0; i < r.active; ++i) t += token_tiles(p, r, i);
+  return t * p.down.row_blocks;
+}
+
 struct Down {
   static constexpr bool kEarlyWeights = true;
-  using Walk = moe::Walk;
+  struct Walk {
+    int i, base;  // active expert i, whose first tile is `base`
+  };
   const Args& p;
   const Routing& r;
+  __device__ __forceinline__ int tiles() const { return down_tiles(p, r); }
   __device__ __forceinline__ Walk start() const { return {0, 0}; }
-  __device__ __forceinline__ int tiles(int i) const {
-    const int n = r.off[i + 1] - r.off[i];
-    return n <= p.down.nb ? 1 : (n + p.down.nb - 1) / p.down.nb;
-  }
-  __device__ __forceinline__ bool span(Walk& w, int u, stream::Span& s) const {
-    const stream::Plan& pl = p.down;
-    const int per = pl.row_blocks * pl.ksplit;
-    if (w.i >= r.active) return false;
-    int t = tiles(w.i);
-    while (u - w.base >= per * t) {
-      w.base += per * t;
-      if (++w.i >= r.active) return false;
-      t = tiles(w.i);
+  __device__ __forceinline__ stream::Tile tile(Walk& w, int t) const {
+    int n = token_tiles(p, r, w.i);
+    while (t - w.base >= p.down.row_blocks * n) {
+      w.base += p.down.row_blocks * n;
+      n = token_tiles(p, r, ++w.i);
     }
-    const int j = u - w.base, b = t == 1 ? j : j / t, rb = b / pl.ksplit, ks = b - rb * pl.ksplit;
-    s.w_row = r.act[w.i] * pl.n + rb * stream::kRows;
-    s.x_row = r.off[w.i] + (j - b * t) * pl.nb;
-    s.kb0 = ks * pl.kbs;
-    s.kb1 = min(pl.num_kb, s.kb0 + pl.kbs);
-    return true;
+    const int j = t - w.base, rb = n == 1 ? j : j / n;
+    return {r.act[w.i] * p.down.n + rb * stream::kRows, r.off[w.i] + (j - rb * n) * p.down.nb};
   }
-  __device__ __forceinline__ void store(const Walk& w, int, const stream::Span& s, uint32_t tmem, int row) const {
+  __device__ __forceinline__ void store(const Walk& w, int, int slice, const stream::Tile& s, uint32_t tmem,
+                                        int row) const {
     const stream::Plan& pl = p.down;
     const int col = s.w_row - r.act[w.i] * pl.n + row, left = r.off[w.i + 1] - s.x_row;
-    int32_t* out = p.part + static_cast<int64_t>(s.kb0 / pl.kbs) * (p.m * p.topk) * pl.n + col;
+    int32_t* out = p.part + static_cast<int64_t>(slice) * (p.m * p.topk) * pl.n + col;
     stream::each_column(tmem, left < pl.nb ? left : pl.nb, [&](int c, int v) {
       if (col < pl.n) out[static_cast<int64_t>(r.pairs[s.x_row + c]) * pl.n] = v;
     });
   }
 };
+
+// What kernels 2 and 4 need of the routing (by all threads).
+__device__ __forceinline__ void write_routing(const Args& p, const Routing& r) {
+  const int tid = threadIdx.x, pairs = p.m * p.topk, total = r.off[r.active];
+  const int up_per = stream::share(r.active * p.up.row_blocks, p.up.num_kb, p.up_grid);
+  const int down_per = stream::share(down_tiles(p, r), p.down.num_kb, p.down_grid);
+  for (int i = total + tid; i < pairs; i += blockDim.x) p.by_pos[i] = make_int4(-1, 0, 0, 0);
+  for (int i = tid; i < pairs; i += blockDim.x)
+    if (expert_of(p, i) < 0) p.by_pair[i] = make_int4(-1, 0, 0, 0);
+  int base = 0;
+  for (int i = 0; i < r.active; ++i) {
+    const int n = token_tiles(p, r, i), e = r.act[i];
+    for (int pos = r.off[i] + tid; pos < r.off[i + 1]; pos += blockDim.x) {
+      const int pair = r.pairs[pos];
+      p.by_pos[pos] = make_int4(pair, e, i * p.up.row_blocks, up_per);
+      p.by_pair[pair] = make_int4(e, base + (pos - r.off[i]) / p.down.nb, n, down_per);
+    }
+    base += n * p.down.row_blocks;
+  }
+}
 
 __global__ void __launch_bounds__(stream::kThreads, 1)
     moe_gate_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
@@ -214,20 +233,17 @@ __global__ void __launch_bounds__(stream::kThreads, 1)
   griddep_launch_dependents();
   uint8_t* ring = stream::ring_of(raw);
   route(p, r, reinterpret_cast<int*>(ring));
-  if (blockIdx.x == 0) {
-    const int* src = reinterpret_cast<const int*>(&r);
-    for (int i = threadIdx.x; i < static_cast<int>(sizeof(Routing) / 4); i += stream::kThreads)
-      reinterpret_cast<int*>(p.routing)[i] = src[i];
-  }
+  if (blockIdx.x == gridDim.x - 1) write_routing(p, r);  // (the last CTA: its share is the smallest)
   fence_proxy_async_smem();  // the scratch above lies where copies will land
   __syncthreads();
   stream::run(GateUp{p, r}, p.up, s, ring, &tmW, &tmX);
   stream::teardown(s);
 }
 
-// What this kernel reads before its wait (the routing, weights) is complete: the
-// quantiser before it has waited for the kernel that wrote the routing, and that
-// one for whatever wrote the caller's data, before this one could start.
+// It may start while kernel 1 runs (kernel 2 lets it, before its own wait).  What
+// it reads before it waits for kernel 2, ids and weights, is the caller's and
+// complete: kernel 1 has waited for whatever wrote them before it let kernel 2
+// start.
 __global__ void __launch_bounds__(stream::kThreads, 1)
     moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                     const __grid_constant__ Args p) {
@@ -238,24 +254,26 @@ __global__ void __launch_bounds__(stream::kThreads, 1)
     prefetch_tmap(&tmW);
     prefetch_tmap(&tmX);
   }
-  for (int i = threadIdx.x; i < static_cast<int>(sizeof(Routing) / 4); i += stream::kThreads)
-    reinterpret_cast<int*>(&r)[i] = __ldcg(reinterpret_cast<const int*>(p.routing) + i);
   stream::setup(s, p.down);
-  stream::run(Down{p, r}, p.down, s, stream::ring_of(raw), &tmW, &tmX);
+  uint8_t* ring = stream::ring_of(raw);
+  route(p, r, reinterpret_cast<int*>(ring));
+  fence_proxy_async_smem();  // the scratch above lies where copies will land
+  __syncthreads();
+  stream::run(Down{p, r}, p.down, s, ring, &tmW, &tmX);
   stream::teardown(s);
 }
 
 // Row `pos` of q: h = silu(g) * u of pair pairs[pos], quantised.  One CTA or
 // cluster per row; a thread keeps up to kQuantVec vectors of 4 values, or, when
 // the row is longer, leaves h in the gate sums' place and reads it back.
-constexpr int kQuantThreads = 256;
+constexpr int kQuantThreads = 512;
 constexpr int kQuantVec = 4;
 
 template <bool CLUSTER, bool LONG>
 __global__ void __launch_bounds__(kQuantThreads) moe_quant_kernel(Args p) {
   __shared__ float red[33];
+  griddep_launch_dependents();  // kernel 3 may take the SMs that kernel 1 leaves
   griddep_wait();
-  griddep_launch_dependents();
   int ranks = 1, rank = 0, pos = blockIdx.x;
   if constexpr (CLUSTER) {
     namespace cg = cooperative_groups;
@@ -263,8 +281,9 @@ __global__ void __launch_bounds__(kQuantThreads) moe_quant_kernel(Args p) {
     rank = static_cast<int>(cg::this_cluster().block_rank());
     pos = blockIdx.x / ranks;
   }
-  if (pos >= p.routing->off[p.routing->active]) return;  // (the whole cluster: slots without an expert)
-  const int pair = p.routing->pairs[pos], e = __ldg(p.ids + pair), pairs = p.m * p.topk;
+  const int4 rec = p.by_pos[pos];
+  if (rec.x < 0) return;  // (the whole cluster: more rows than pairs with an expert)
+  const int pair = rec.x, e = rec.y, pairs = p.m * p.topk;
   const float sa = __ldg(p.sa + ((pair * p.topk_inv) >> 16));
   int32_t* gu = p.gu + static_cast<int64_t>(pair) * 2 * p.inter;
   const int64_t slice = static_cast<int64_t>(pairs) * 2 * p.inter;
@@ -272,7 +291,8 @@ __global__ void __launch_bounds__(kQuantThreads) moe_quant_kernel(Args p) {
   const int nvec = p.inter / 4, stride = ranks * kQuantThreads, t0 = rank * kQuantThreads + threadIdx.x;
   auto sums = [&](int at) {
     int4 v = *reinterpret_cast<const int4*>(gu + at);
-    for (int k = 1; k < p.up.ksplit; ++k) {
+    const int n = stream::slices_of(rec.z + at / stream::kRows, p.up.num_kb, rec.w);
+    for (int k = 1; k < n; ++k) {
       const int4 o = *reinterpret_cast<const int4*>(gu + k * slice + at);
       v.x += o.x;
       v.y += o.y;
@@ -283,16 +303,11 @@ __global__ void __launch_bounds__(kQuantThreads) moe_quant_kernel(Args p) {
   };
   auto row4 = [&](int j, float (&h)[4]) {
     const int4 g = sums(j), u = sums(p.inter + j);
-    float a[4], b[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int gi = i == 0 ? g.x : (i == 1 ? g.y : (i == 2 ? g.z : g.w));
-      const int ui = i == 0 ? u.x : (i == 1 ? u.y : (i == 2 ? u.z : u.w));
-      a[i] = __fmul_rn(__fmul_rn(__int2float_rn(gi), sa), __ldg(s13 + j + i));
-      b[i] = __fmul_rn(__fmul_rn(__int2float_rn(ui), sa), __ldg(s13 + p.inter + j + i));
-    }
-    quant::silu_mul2(a[0], a[1], b[0], b[1], h[0], h[1]);
-    quant::silu_mul2(a[2], a[3], b[2], b[3], h[2], h[3]);
+    const float4 sg = __ldg(reinterpret_cast<const float4*>(s13 + j));
+    const float4 su = __ldg(reinterpret_cast<const float4*>(s13 + p.inter + j));
+    auto val = [&](int acc, float sw) { return __fmul_rn(__fmul_rn(__int2float_rn(acc), sa), sw); };
+    quant::silu_mul2(val(g.x, sg.x), val(g.y, sg.y), val(u.x, su.x), val(u.y, su.y), h[0], h[1]);
+    quant::silu_mul2(val(g.z, sg.z), val(g.w, sg.w), val(u.z, su.z), val(u.w, su.w), h[2], h[3]);
   };
   float h[LONG ? 1 : kQuantVec][4], amax = 0.0f;
   if constexpr (LONG) {
@@ -337,33 +352,49 @@ __global__ void __launch_bounds__(kQuantThreads) moe_quant_kernel(Args p) {
   if constexpr (CLUSTER) quant::cluster_arrive_wait_relaxed();  // peers may still read red[32]
 }
 
-// out[i][j .. j + 3]: the slots in order.
+// out[i][j .. j + 3]: the slots in order, four at a time.  The loads of all four
+// are issued before any is used, of slots without an expert too (their rows of
+// the workspace hold anything, and are not used): one slot after another, each
+// waiting for its own chain of loads, took 8 us for 6 slots of 4 tokens.
 __global__ void __launch_bounds__(128) moe_combine_kernel(Args p) {
+  constexpr int S = 4;
   griddep_wait();
   griddep_launch_dependents();
   const int i = blockIdx.y, j = (blockIdx.x * 128 + threadIdx.x) * 4;
   if (j >= p.hidden) return;
   const int64_t slice = static_cast<int64_t>(p.m) * p.topk * p.hidden;
   float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-  for (int s = 0; s < p.topk; ++s) {
-    const int pair = i * p.topk + s, e = expert_of(p, pair);
-    if (e >= 0) {
-      const int32_t* part = p.part + static_cast<int64_t>(pair) * p.hidden + j;
-      int4 acc = __ldg(reinterpret_cast<const int4*>(part));
-      for (int k = 1; k < p.down.ksplit; ++k) {
+  for (int s0 = 0; s0 < p.topk; s0 += S) {
+    int4 rec[S], acc[S];
+    float4 s2[S];
+    float sh[S], wt[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const int pair = i * p.topk + min(s0 + s, p.topk - 1);
+      rec[s] = __ldg(p.by_pair + pair);
+      acc[s] = __ldg(reinterpret_cast<const int4*>(p.part + static_cast<int64_t>(pair) * p.hidden + j));
+      sh[s] = __ldg(p.sh + pair);
+      wt[s] = __ldg(p.wt + pair);
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+      s2[s] = __ldg(reinterpret_cast<const float4*>(p.s2 + static_cast<int64_t>(max(rec[s].x, 0)) * p.hidden + j));
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      if (s0 + s >= p.topk || rec[s].x < 0) continue;
+      const int32_t* part = p.part + (static_cast<int64_t>(i) * p.topk + s0 + s) * p.hidden + j;
+      const int n = stream::slices_of(rec[s].y + j / stream::kRows * rec[s].z, p.down.num_kb, rec[s].w);
+      for (int k = 1; k < n; ++k) {
         const int4 v = __ldg(reinterpret_cast<const int4*>(part + k * slice));
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
+        acc[s].x += v.x;
+        acc[s].y += v.y;
+        acc[s].z += v.z;
+        acc[s].w += v.w;
       }
-      const float* s2 = p.s2 + static_cast<int64_t>(e) * p.hidden + j;
-      const float sh = __ldg(p.sh + pair), wt = __ldg(p.wt + pair);
-      f[0] = __fmaf_rn(wt, __fmul_rn(__fmul_rn(__int2float_rn(acc.x), sh), __ldg(s2)), f[0]);
-      f[1] = __fmaf_rn(wt, __fmul_rn(__fmul_rn(__int2float_rn(acc.y), sh), __ldg(s2 + 1)), f[1]);
-      f[2] = __fmaf_rn(wt, __fmul_rn(__fmul_rn(__int2float_rn(acc.z), sh), __ldg(s2 + 2)), f[2]);
-      f[3] = __fmaf_rn(wt, __fmul_rn(__fmul_rn(__int2float_rn(acc.w), sh), __ldg(s2 + 3)), f[3]);
+      f[0] = __fmaf_rn(wt[s], __fmul_rn(__fmul_rn(__int2float_rn(acc[s].x), sh[s]), s2[s].x), f[0]);
+      f[1] = __fmaf_rn(wt[s], __fmul_rn(__fmul_rn(__int2float_rn(acc[s].y), sh[s]), s2[s].y), f[1]);
+      f[2] = __fmaf_rn(wt[s], __fmul_rn(__fmul_rn(__int2float_rn(acc[s].z), sh[s]), s2[s].z), f[2]);
+      f[3] = __fmaf_rn(wt[s], __fmul_rn(__fmul_rn(__int2float_rn(acc[s].w), sh[s]), s2[s].w), f[3]);
     }
   }
   const int64_t o = static_cast<int64_t>(i) * p.hidden + j;
@@ -374,21 +405,20 @@ __global__ void __launch_bounds__(128) moe_combine_kernel(Args p) {
     *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) = make_float4(f[0], f[1], f[2], f[3]);
 }
 
-// Both products' plans.  Experts expected in use: no more than there are pairs.
-// Tokens of a down unit: twice an expert's share of the pairs where the router
-// spreads them evenly; an expert with more has its weights read again, from L2.
-inline void plans(int m, int hidden, int inter, int experts, int topk, int num_sms, stream::Plan* up,
-                  stream::Plan* down) {
-  const int64_t pairs = static_cast<int64_t>(m) * topk, sets = pairs < experts ? pairs : experts;
-  *up = stream::plan(m, sets, 2 * inter, hidden, num_sms);
-  const int64_t share = (2 * pairs + experts - 1) / experts;
-  *down = stream::plan(static_cast<int>(share < m ? share : m), sets, hidden, inter, num_sms);
+// Both products' plans.  Tokens of a down tile: twice an expert's share of the
+// pairs where the router spreads them evenly; an expert with more has its
+// weights read again, from L2.
+inline void plans(Args& a, int num_sms) {
+  const int64_t pairs = static_cast<int64_t>(a.m) * a.topk, share = (2 * pairs + a.experts - 1) / a.experts;
+  a.up = stream::plan(a.m, 2 * a.inter, a.hidden, num_sms);
+  a.down = stream::plan(static_cast<int>(share < a.m ? share : a.m), a.hidden, a.inter, num_sms);
+  a.up_grid = a.down_grid = num_sms;
 }
 
 inline cudaError_t launch_quant(const Args& a, int num_sms, cudaStream_t stream) {
   const int pairs = a.m * a.topk, per = kQuantThreads * kQuantVec * 4;  // values a CTA holds
   int cl = 1;
-  while (cl < 8 && (a.inter > cl * per || (pairs * cl < 2 * num_sms && a.inter > cl * kQuantThreads * 4))) cl *= 2;
+  while (cl < 8 && (a.inter > cl * per || (2 * pairs * cl <= num_sms && a.inter > cl * kQuantThreads * 4))) cl *= 2;
   const dim3 grid(static_cast<unsigned>(pairs * cl)), block(kQuantThreads);
   if (a.inter > cl * per)
     return launch_pdl(moe_quant_kernel<true, true>, grid, block, 0, stream, static_cast<unsigned>(cl), a);
@@ -410,17 +440,12 @@ inline int launch(const Args& a, const int8_t* x, const int8_t* w13, const int8_
   const size_t most = stream::kRingBytes + 1024;
   if ((*err = gemm::set_smem_once(moe_gate_up_kernel, dev, 0, most)) != cudaSuccess) return 2;
   if ((*err = gemm::set_smem_once(moe_down_kernel, dev, 1, most)) != cudaSuccess) return 2;
-  // units at most: every active expert's, and in the down product one token tile
-  // more for every nb pairs
-  const int64_t sets = pairs < a.experts ? pairs : a.experts;
-  const int64_t up = sets * a.up.row_blocks * a.up.ksplit;
-  const int64_t down = (sets + pairs / a.down.nb) * a.down.row_blocks * a.down.ksplit;
-  *err = launch_pdl(moe_gate_up_kernel, dim3(static_cast<unsigned>(up < num_sms ? up : num_sms)),
-                    dim3(stream::kThreads), stream::smem_bytes(a.up), stream, 1, tw13, tx, a);
+  *err = launch_pdl(moe_gate_up_kernel, dim3(a.up_grid), dim3(stream::kThreads), stream::smem_bytes(a.up), stream, 1,
+                    tw13, tx, a);
   if (*err == cudaSuccess) *err = launch_quant(a, num_sms, stream);
   if (*err == cudaSuccess)
-    *err = launch_pdl(moe_down_kernel, dim3(static_cast<unsigned>(down < num_sms ? down : num_sms)),
-                      dim3(stream::kThreads), stream::smem_bytes(a.down), stream, 1, tw2, tq, a);
+    *err = launch_pdl(moe_down_kernel, dim3(a.down_grid), dim3(stream::kThreads), stream::smem_bytes(a.down), stream,
+                      1, tw2, tq, a);
   if (*err == cudaSuccess)
     *err = launch_pdl(moe_combine_kernel, dim3((a.hidden + 511) / 512, a.m), dim3(128), 0, stream, 1, a);
   return *err == cudaSuccess ? 0 : 2;

@@ -745,24 +745,39 @@ qk_status qk_w8a8_lora_gemm(int m, int n, int k, const int8_t* a, const int8_t* 
   return cuda_status(lora::launch_expand(la, dev->sms, s), "adapter expand launch");
 }
 
-// ---- a MoE layer for a few tokens; the workspace holds the routing, the gate
+// ---- a MoE layer for a few tokens; the workspace holds the sorted pairs, the gate
 // and up sums, the down sums, the scales of h and its int8 values
 namespace {
 constexpr int kMoeLayerTokens = 64, kMoeLayerTopk = 32, kMoeLayerExperts = moe::kMaxExperts;
 
 struct MoeLayout {
-  size_t gu, part, sh, q, total;  // byte offsets (the routing is at 0)
+  size_t by_pos, by_pair, gu, part, sh, q, total;  // byte offsets; by_pos is at 0
 };
 
-MoeLayout moe_layout(int m, int hidden, int inter, int topk, const stream::Plan& up, const stream::Plan& down) {
-  const size_t pairs = static_cast<size_t>(m) * topk;
+MoeLayout moe_layout(const moe::Args& a) {
+  const size_t pairs = static_cast<size_t>(a.m) * a.topk;
   MoeLayout l;
-  l.gu = round256(sizeof(moe::Routing));
-  l.part = l.gu + round256(pairs * inter * 8 * up.ksplit);
-  l.sh = l.part + round256(pairs * hidden * 4 * down.ksplit);
+  l.by_pos = 0;
+  l.by_pair = round256(pairs * 16);
+  l.gu = l.by_pair + round256(pairs * 16);
+  l.part = l.gu + round256(pairs * a.inter * 8 * a.up.max_slices);
+  l.sh = l.part + round256(pairs * a.hidden * 4 * a.down.max_slices);
   l.q = l.sh + round256(pairs * 4);
-  l.total = l.q + round256(pairs * inter);
+  l.total = l.q + round256(pairs * a.inter);
   return l;
+}
+
+// The sizes and the plans that follow from them.
+moe::Args moe_args(int m, int hidden, int inter, int num_experts, int topk, int num_sms) {
+  moe::Args a = {};
+  a.m = m;
+  a.hidden = hidden;
+  a.inter = inter;
+  a.experts = num_experts;
+  a.topk = topk;
+  a.topk_inv = (65536 + topk - 1) / topk;
+  moe::plans(a, num_sms);
+  return a;
 }
 
 qk_status moe_layer_check(int m, int hidden, int inter, int num_experts, int topk) {
@@ -773,6 +788,9 @@ qk_status moe_layer_check(int m, int hidden, int inter, int num_experts, int top
   if (static_cast<int64_t>(num_experts) * 2 * inter > INT32_MAX ||
       static_cast<int64_t>(num_experts) * hidden > INT32_MAX)
     return QK_ERR_INVALID_ARG;
+  // (so that a product has at most 2^31 / 128 tiles and one more for each expert
+  // and each pair, of at most 1041 K blocks: under 2^32 blocks with the pairs'
+  // 2048 and the experts' 1024 row-block remainders)
   if (m > kMoeLayerTokens || topk > kMoeLayerTopk || num_experts > kMoeLayerExperts) return QK_ERR_UNSUPPORTED;
   return QK_OK;
 }
@@ -782,9 +800,7 @@ size_t qk_w8a8_moe_layer_workspace_size(int m, int hidden, int inter, int num_ex
   const DeviceInfo* dev = nullptr;
   if (moe_layer_check(m, hidden, inter, num_experts, topk) != QK_OK || m == 0 || check_device(&dev) != QK_OK)
     return 0;
-  stream::Plan up, down;
-  moe::plans(m, hidden, inter, num_experts, topk, dev->sms, &up, &down);
-  return moe_layout(m, hidden, inter, topk, up, down).total;
+  return moe_layout(moe_args(m, hidden, inter, num_experts, topk, dev->sms)).total;
 }
 
 qk_status qk_w8a8_moe_layer(int m, int hidden, int inter, int num_experts, int topk, const int8_t* a,
@@ -802,28 +818,22 @@ qk_status qk_w8a8_moe_layer(int m, int hidden, int inter, int num_experts, int t
     return QK_ERR_INVALID_ARG;
   if (!aligned(a, 16) || !aligned(w_gate_up, 16) || !aligned(w_down, 16) || !aligned(out, 16) ||
       !aligned(scale_a, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) ||
-      !aligned(scale_gate_up, 4) || !aligned(scale_down, 4))
+      !aligned(scale_gate_up, 16) || !aligned(scale_down, 16))
     return QK_ERR_MISALIGNED;
   const DeviceInfo* dev = nullptr;
   st = check_device(&dev);
   if (st != QK_OK) return st;
-  moe::Args g = {};
-  moe::plans(m, hidden, inter, num_experts, topk, dev->sms, &g.up, &g.down);
-  const MoeLayout l = moe_layout(m, hidden, inter, topk, g.up, g.down);
+  moe::Args g = moe_args(m, hidden, inter, num_experts, topk, dev->sms);
+  const MoeLayout l = moe_layout(g);
   if (workspace == nullptr || workspace_bytes < l.total || !aligned(workspace, 256)) return QK_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
-  g.m = m;
-  g.hidden = hidden;
-  g.inter = inter;
-  g.experts = num_experts;
-  g.topk = topk;
-  g.topk_inv = (65536 + topk - 1) / topk;
   g.sa = scale_a;
   g.ids = topk_ids;
   g.wt = topk_weights;
   g.s13 = scale_gate_up;
   g.s2 = scale_down;
-  g.routing = reinterpret_cast<moe::Routing*>(ws);
+  g.by_pos = reinterpret_cast<int4*>(ws + l.by_pos);
+  g.by_pair = reinterpret_cast<int4*>(ws + l.by_pair);
   g.gu = reinterpret_cast<int32_t*>(ws + l.gu);
   g.part = reinterpret_cast<int32_t*>(ws + l.part);
   g.sh = reinterpret_cast<float*>(ws + l.sh);

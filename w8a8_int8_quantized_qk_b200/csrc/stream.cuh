@@ -11,9 +11,10 @@
 // of the pipe at full HBM rate for 8 tokens and the bound beyond 16, and its
 // chains of dependent products kept 8 tokens of 2 experts at 4.9 TB/s.
 //
-// The sums leave as int32, one slice for each K range a unit is cut into (so
-// that few row blocks still occupy every SM); what reads them adds the slices,
-// exactly.
+// Every CTA takes the same number of 128 x 128-byte blocks, in the order of
+// the tiles (128 rows by all of K), so no SM idles in a last round: a tile that
+// two CTAs share leaves as two partial sums.  The sums are int32, one slice for
+// each part a tile is cut into; what reads them adds the slices, exactly.
 #pragma once
 
 #include "gemm_sm100.cuh"
@@ -31,22 +32,39 @@ constexpr int kTmemCols = 128;     // two accumulators of 64 columns
 constexpr size_t kRingBytes = 212 * 1024;
 
 struct Plan {
-  int nb;        // tokens of a unit: 16, 32, 48 or 64
+  int nb;          // tokens of a tile: 16, 32, 48 or 64
   int stages;
-  int num_kb;    // K blocks of a row
-  int ksplit;    // K ranges
-  int kbs;       // K blocks of a range (the last may have fewer)
+  int num_kb;      // K blocks of a tile
   int row_blocks;
-  int n;         // weight rows (per expert)
+  int n;           // weight rows (per expert)
+  int max_slices;  // parts a tile is cut into, at most
 };
 
 __host__ __device__ inline int stage_bytes(int nb) { return kRows * kK + nb * kK; }
 
-// `tokens`: N side wanted; `sets`: independent sets of n rows (experts).  K is
-// cut until there are about five units an SM, no range shorter than four
-// blocks: an uneven last round then costs a fifth of the time at most, and in
-// fact less, since an SM streams faster while others have ended.
-inline Plan plan(int tokens, int64_t sets, int n, int k, int num_sms) {
+// Blocks a CTA takes of `tiles` tiles: an equal share, but no fewer than four
+// (64 KB) and no more than eight parts to a tile.
+__host__ __device__ inline int share(int tiles, int num_kb, int grid) {
+  const int64_t all = static_cast<int64_t>(tiles) * num_kb;
+  int per = static_cast<int>((all + grid - 1) / grid);
+  if (per < 4) per = 4;
+  const int least = (num_kb + 7) / 8;
+  return per < least ? least : per;
+}
+
+// Slices of a tile, and the slice of the part that CTA `bid` holds of it.  (The
+// host has checked that all blocks together are fewer than 2^32.)
+__device__ __forceinline__ int slices_of(int tile, int num_kb, int per) {
+  const uint32_t f = static_cast<uint32_t>(tile) * num_kb, d = static_cast<uint32_t>(per);
+  return static_cast<int>((f + num_kb - 1) / d - f / d) + 1;
+}
+__device__ __forceinline__ int slice_of(int tile, int num_kb, int per, int bid) {
+  return bid - static_cast<int>(static_cast<uint32_t>(tile) * num_kb / static_cast<uint32_t>(per));
+}
+
+// `tokens`: N side wanted of sets of n rows (experts) by k.  The grid is one
+// CTA an SM; the fewest blocks a CTA can get, those of one set, bound the slices.
+inline Plan plan(int tokens, int n, int k, int num_sms) {
   Plan p;
   p.nb = tokens >= kMaxTokens ? kMaxTokens : (tokens + 15) / 16 * 16;
   const int fit = static_cast<int>(kRingBytes / stage_bytes(p.nb));
@@ -54,11 +72,9 @@ inline Plan plan(int tokens, int64_t sets, int n, int k, int num_sms) {
   p.num_kb = (k + kK - 1) / kK;
   p.row_blocks = (n + kRows - 1) / kRows;
   p.n = n;
-  p.ksplit = 1;
-  while (p.ksplit < 8 && sets * p.row_blocks * p.ksplit < 5LL * num_sms && p.num_kb / (2 * p.ksplit) >= 4)
-    p.ksplit *= 2;
-  p.kbs = (p.num_kb + p.ksplit - 1) / p.ksplit;
-  p.ksplit = (p.num_kb + p.kbs - 1) / p.kbs;
+  const int per = share(p.row_blocks, p.num_kb, num_sms);
+  // a part starts at the tile's start or at a multiple of `per` inside it
+  p.max_slices = (p.num_kb - 1) / per + 2;
   return p;
 }
 
@@ -74,10 +90,9 @@ struct Bars {
   int abort;
 };
 
-// One unit: 128 weight rows, a K range and the tokens they meet.
-struct Span {
-  int w_row, x_row;  // first rows in the two tensor maps
-  int kb0, kb1;
+// A tile in the two tensor maps.
+struct Tile {
+  int w_row, x_row;
 };
 
 __device__ __forceinline__ uint32_t tmem_ld_x1(uint32_t taddr) {
@@ -86,40 +101,66 @@ __device__ __forceinline__ uint32_t tmem_ld_x1(uint32_t taddr) {
   return r;
 }
 
+// The blocks [f, end) of a CTA, tile by tile.
+struct Range {
+  uint32_t f, end;
+  __device__ __forceinline__ Range(int tiles, int num_kb, int per) {
+    const uint64_t all = static_cast<uint64_t>(tiles) * num_kb, at = static_cast<uint64_t>(blockIdx.x) * per;
+    f = static_cast<uint32_t>(at < all ? at : all);
+    end = static_cast<uint32_t>(at + per < all ? at + per : all);
+  }
+  // the part of the next tile: K blocks [kb0, kb1)
+  __device__ __forceinline__ bool next(int num_kb, int& tile, int& kb0, int& kb1) {
+    if (f >= end) return false;
+    tile = static_cast<int>(f / static_cast<uint32_t>(num_kb));
+    kb0 = static_cast<int>(f - static_cast<uint32_t>(tile) * num_kb);
+    const int left = static_cast<int>(end - f);
+    kb1 = left < num_kb - kb0 ? kb0 + left : num_kb;
+    f += kb1 - kb0;
+    return true;
+  }
+};
+
 // The roles.  P has:
 //   static constexpr bool kEarlyWeights   the first weights are requested before
 //                                     the wait for the previous kernel (which must
 //                                     not write them)
-//   Walk start(); bool span(Walk&, int u, Span&)   unit u (a Walk goes upward
-//                                     only); false past the last
-//   void store(Walk&, int u, const Span&, uint32_t tmem, int row)   unit u's sums:
-//                                     row `row` of the unit, tokens in TMEM columns
+//   int tiles()
+//   Walk start(); Tile tile(Walk&, int t)   tile t (a Walk goes upward only)
+//   void store(Walk, int t, int slice, Tile, uint32_t tmem, int row)   a part's
+//                                     sums: row `row` of the tile, tokens in TMEM
+//                                     columns
 template <class P>
 __device__ __forceinline__ void run(const P& prob, const Plan& pl, Bars& s, uint8_t* ring, const CUtensorMap* tmW,
                                     const CUtensorMap* tmX) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int stages = pl.stages, sb = stage_bytes(pl.nb);
-  const int bid = static_cast<int>(blockIdx.x), grid = static_cast<int>(gridDim.x);
+  const int stages = pl.stages, sb = stage_bytes(pl.nb), num_kb = pl.num_kb;
+  const int tiles = prob.tiles(), per = share(tiles, num_kb, static_cast<int>(gridDim.x));
   const uint32_t ring0 = smem_addr(ring);
+  Range parts(tiles, num_kb, per);
+  typename P::Walk w = prob.start();
+  int t, kb0, kb1;
   if (warp == 0) {
     if (lane == 0) {
       int stage = 0, pre = 0;
       uint32_t phase = 0, issued = 0;
       bool ok = true;
-      typename P::Walk w = prob.start();
-      Span u;
       if constexpr (P::kEarlyWeights) {
+        Range early = parts;
         typename P::Walk we = prob.start();
-        for (int unit = bid; pre < stages && prob.span(we, unit, u); unit += grid)
-          for (int kb = u.kb0; kb < u.kb1 && pre < stages; ++kb, ++pre) {
+        while (pre < stages && early.next(num_kb, t, kb0, kb1)) {
+          const Tile u = prob.tile(we, t);
+          for (int kb = kb0; kb < kb1 && pre < stages; ++kb, ++pre) {
             const uint32_t fb = smem_addr(&s.full[pre]);
             mbar_arrive_expect_tx(fb, static_cast<uint32_t>(sb));
             tma_load_2d(ring0 + pre * sb, tmW, fb, kb * kK, u.w_row);
           }
+        }
         griddep_wait();
       }
-      for (int unit = bid; ok && prob.span(w, unit, u); unit += grid) {
-        for (int kb = u.kb0; kb < u.kb1; ++kb) {
+      while (ok && parts.next(num_kb, t, kb0, kb1)) {
+        const Tile u = prob.tile(w, t);
+        for (int kb = kb0; kb < kb1; ++kb) {
           const uint32_t fb = smem_addr(&s.full[stage]);
           if (pre > 0) {
             --pre;  // this stage's weights are on their way
@@ -157,13 +198,11 @@ __device__ __forceinline__ void run(const P& prob, const Plan& pl, Bars& s, uint
       int stage = 0;
       uint32_t phase = 0, abuf = 0, aphase = 0;
       bool ok = true;
-      typename P::Walk w = prob.start();
-      Span u;
-      for (int unit = bid; ok && prob.span(w, unit, u); unit += grid) {
+      while (ok && parts.next(num_kb, t, kb0, kb1)) {
         if (!mbar_wait(smem_addr(&s.acc_empty[abuf]), aphase ^ 1u, &s.abort)) break;
         tc_fence_after();
         const uint32_t d = s.tmem_base + abuf * kMaxTokens;
-        for (int kb = u.kb0; kb < u.kb1; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait(smem_addr(&s.full[stage]), phase, &s.abort)) {
             ok = false;
             break;
@@ -173,7 +212,7 @@ __device__ __forceinline__ void run(const P& prob, const Plan& pl, Bars& s, uint
 #pragma unroll
           for (int kk = 0; kk < kK / gemm::UMMA_K; ++kk)
             mma_i8(d, sdesc_k_sw128(a0 + kk * gemm::UMMA_K), sdesc_k_sw128(b0 + kk * gemm::UMMA_K), idesc,
-                   kb > u.kb0 || kk > 0);
+                   kb > kb0 || kk > 0);
           mma_commit(smem_addr(&s.empty[stage]));
           if (++stage == stages) {
             stage = 0;
@@ -198,13 +237,12 @@ __device__ __forceinline__ void run(const P& prob, const Plan& pl, Bars& s, uint
     }
     const int quad = warp & 3;
     uint32_t abuf = 0, aphase = 0;
-    typename P::Walk w = prob.start();
-    Span u;
-    for (int unit = bid; prob.span(w, unit, u); unit += grid) {
+    while (parts.next(num_kb, t, kb0, kb1)) {
+      const Tile u = prob.tile(w, t);
       if (!gemm::warp_wait(smem_addr(&s.acc_full[abuf]), aphase, &s.abort)) break;
       tc_fence_after();
-      prob.store(w, unit, u, s.tmem_base + abuf * kMaxTokens + (static_cast<uint32_t>(quad * 32) << 16),
-                 quad * 32 + lane);
+      prob.store(w, t, slice_of(t, num_kb, per, static_cast<int>(blockIdx.x)), u,
+                 s.tmem_base + abuf * kMaxTokens + (static_cast<uint32_t>(quad * 32) << 16), quad * 32 + lane);
       tc_fence_before();
       if (lane == 0) mbar_arrive(smem_addr(&s.acc_empty[abuf]));
       abuf ^= 1u;
