@@ -17,7 +17,8 @@
 //      weights), keeping the columns of an expert's own tokens, so that no token
 //      is gathered or copied;
 //   2. scales, silu, the row's maximum and its quantisation, one CTA or cluster
-//      per pair, into rows sorted by expert;
+//      per pair, into rows sorted by expert; it starts beside kernel 1 and has
+//      its place and its scales in hand when that ends;
 //   3. the down rows past each expert's rows; a CTA starts, sorts the pairs and
 //      requests its first 180 KB of weights as soon as one of kernel 1 has left
 //      its SM, while the others and kernel 2 still run;
@@ -50,10 +51,8 @@ struct Args {
   const float* wt;      // [m, topk]
   const float* s13;     // [experts, 2 inter]
   const float* s2;      // [experts, hidden]
-  int4* by_pos;         // workspace, like the following; [pairs]: {pair, expert, first tile of gate and up, blocks of a CTA there}, pair -1 past
-                        // the last, in the sorted order
-  int4* by_pair;        // [pairs]: {expert or -1, first tile of the down product, tiles from one row block to the
-                        // next, blocks of a CTA there}
+  int4* by_pair;        // workspace, like the following; [pairs]: {expert or -1, first tile of the down product,
+                        // tiles from one row block to the next, blocks of a CTA there}
   int32_t* gu;          // [slices, pairs, 2 inter]: the gate and up sums
   int8_t* q;            // [pairs, inter], sorted by expert
   float* sh;            // [pairs]
@@ -198,22 +197,17 @@ struct Down {
   }
 };
 
-// What kernels 2 and 4 need of the routing (by all threads).
+// What kernel 4 needs of the routing (by all threads).
 __device__ __forceinline__ void write_routing(const Args& p, const Routing& r) {
-  const int tid = threadIdx.x, pairs = p.m * p.topk, total = r.off[r.active];
-  const int up_per = stream::share(r.active * p.up.row_blocks, p.up.num_kb, p.up_grid);
-  const int down_per = stream::share(down_tiles(p, r), p.down.num_kb, p.down_grid);
-  for (int i = total + tid; i < pairs; i += blockDim.x) p.by_pos[i] = make_int4(-1, 0, 0, 0);
+  const int tid = threadIdx.x, pairs = p.m * p.topk;
+  const int per = stream::share(down_tiles(p, r), p.down.num_kb, p.down_grid);
   for (int i = tid; i < pairs; i += blockDim.x)
     if (expert_of(p, i) < 0) p.by_pair[i] = make_int4(-1, 0, 0, 0);
   int base = 0;
   for (int i = 0; i < r.active; ++i) {
-    const int n = token_tiles(p, r, i), e = r.act[i];
-    for (int pos = r.off[i] + tid; pos < r.off[i + 1]; pos += blockDim.x) {
-      const int pair = r.pairs[pos];
-      p.by_pos[pos] = make_int4(pair, e, i * p.up.row_blocks, up_per);
-      p.by_pair[pair] = make_int4(e, base + (pos - r.off[i]) / p.down.nb, n, down_per);
-    }
+    const int n = token_tiles(p, r, i);
+    for (int pos = r.off[i] + tid; pos < r.off[i + 1]; pos += blockDim.x)
+      p.by_pair[r.pairs[pos]] = make_int4(r.act[i], base + (pos - r.off[i]) / p.down.nb, n, per);
     base += n * p.down.row_blocks;
   }
 }
@@ -263,35 +257,55 @@ __global__ void __launch_bounds__(stream::kThreads, 1)
   stream::teardown(s);
 }
 
-// Row `pos` of q: h = silu(g) * u of pair pairs[pos], quantised.  One CTA or
-// cluster per row; a thread keeps up to kQuantVec vectors of 4 values, or, when
-// the row is longer, leaves h in the gate sums' place and reads it back.
-constexpr int kQuantThreads = 512;
+// A pair's row of q: h = silu(g) * u, quantised.  One CTA or cluster per pair; a
+// thread keeps kQuantVec vectors of 4 values, or, when the row is longer than
+// that, leaves h in the gate sums' place and reads it back.  The row's place
+// among the sorted pairs, how its sums are cut and its scales do not depend on
+// kernel 1: they are found while that runs.
+constexpr int kQuantThreads = 256;
 constexpr int kQuantVec = 4;
 
 template <bool CLUSTER, bool LONG>
 __global__ void __launch_bounds__(kQuantThreads) moe_quant_kernel(Args p) {
   __shared__ float red[33];
+  __shared__ unsigned used[kMaxExperts / 32];
+  __shared__ int place;
   griddep_launch_dependents();  // kernel 3 may take the SMs that kernel 1 leaves
-  griddep_wait();
-  int ranks = 1, rank = 0, pos = blockIdx.x;
+  int ranks = 1, rank = 0, pair = blockIdx.x;
   if constexpr (CLUSTER) {
     namespace cg = cooperative_groups;
     ranks = static_cast<int>(cg::this_cluster().num_blocks());
     rank = static_cast<int>(cg::this_cluster().block_rank());
-    pos = blockIdx.x / ranks;
+    pair = blockIdx.x / ranks;
   }
-  const int4 rec = p.by_pos[pos];
-  if (rec.x < 0) return;  // (the whole cluster: more rows than pairs with an expert)
-  const int pair = rec.x, e = rec.y, pairs = p.m * p.topk;
+  const int tid = threadIdx.x, pairs = p.m * p.topk, e = expert_of(p, pair);
+  if (e < 0) return;  // (the whole cluster)
+  // (ids and scales are the caller's: complete before kernel 1 let this one start)
+  if (tid < kMaxExperts / 32) used[tid] = 0;
+  if (tid == 0) place = 0;
+  __syncthreads();
+  int before = 0;
+  for (int j = tid; j < pairs; j += kQuantThreads) {
+    const int o = expert_of(p, j);
+    if (o >= 0) atomicOr(&used[o >> 5], 1u << (o & 31));
+    before += (o >= 0 && (o < e || (o == e && j < pair))) ? 1 : 0;
+  }
+  before = __reduce_add_sync(0xFFFFFFFFu, before);
+  if ((tid & 31) == 0 && before > 0) atomicAdd(&place, before);
+  __syncthreads();
+  int active = 0, index = 0;  // experts in use, and among them those below e
+  for (int i = 0; i < (p.experts + 31) / 32; ++i) {
+    active += __popc(used[i]);
+    index += i < (e >> 5) ? __popc(used[i]) : (i == (e >> 5) ? __popc(used[i] & ((1u << (e & 31)) - 1u)) : 0);
+  }
+  const int per = stream::share(active * p.up.row_blocks, p.up.num_kb, p.up_grid);
   const float sa = __ldg(p.sa + ((pair * p.topk_inv) >> 16));
   int32_t* gu = p.gu + static_cast<int64_t>(pair) * 2 * p.inter;
   const int64_t slice = static_cast<int64_t>(pairs) * 2 * p.inter;
   const float* s13 = p.s13 + static_cast<int64_t>(e) * 2 * p.inter;
-  const int nvec = p.inter / 4, stride = ranks * kQuantThreads, t0 = rank * kQuantThreads + threadIdx.x;
-  auto sums = [&](int at) {
-    int4 v = *reinterpret_cast<const int4*>(gu + at);
-    const int n = stream::slices_of(rec.z + at / stream::kRows, p.up.num_kb, rec.w);
+  const int nvec = p.inter / 4, stride = ranks * kQuantThreads, t0 = rank * kQuantThreads + tid;
+  auto add_slices = [&](int4& v, int at) {
+    const int n = stream::slices_of(index * p.up.row_blocks + at / stream::kRows, p.up.num_kb, per);
     for (int k = 1; k < n; ++k) {
       const int4 o = *reinterpret_cast<const int4*>(gu + k * slice + at);
       v.x += o.x;
@@ -299,30 +313,48 @@ __global__ void __launch_bounds__(kQuantThreads) moe_quant_kernel(Args p) {
       v.z += o.z;
       v.w += o.w;
     }
-    return v;
   };
-  auto row4 = [&](int j, float (&h)[4]) {
-    const int4 g = sums(j), u = sums(p.inter + j);
-    const float4 sg = __ldg(reinterpret_cast<const float4*>(s13 + j));
-    const float4 su = __ldg(reinterpret_cast<const float4*>(s13 + p.inter + j));
+  auto silu4 = [&](const int4& g, const int4& u, const float4& sg, const float4& su, float (&h)[4]) {
     auto val = [&](int acc, float sw) { return __fmul_rn(__fmul_rn(__int2float_rn(acc), sa), sw); };
     quant::silu_mul2(val(g.x, sg.x), val(g.y, sg.y), val(u.x, su.x), val(u.y, su.y), h[0], h[1]);
     quant::silu_mul2(val(g.z, sg.z), val(g.w, sg.w), val(u.z, su.z), val(u.w, su.w), h[2], h[3]);
   };
+  auto scales4 = [&](int at) { return __ldg(reinterpret_cast<const float4*>(s13 + at)); };
   float h[LONG ? 1 : kQuantVec][4], amax = 0.0f;
   if constexpr (LONG) {
+    griddep_wait();
     for (int v = t0; v < nvec; v += stride) {
-      row4(v * 4, h[0]);
+      int4 g = *reinterpret_cast<const int4*>(gu + v * 4), u = *reinterpret_cast<const int4*>(gu + p.inter + v * 4);
+      add_slices(g, v * 4);
+      add_slices(u, p.inter + v * 4);
+      silu4(g, u, scales4(v * 4), scales4(p.inter + v * 4), h[0]);
       *reinterpret_cast<float4*>(gu + v * 4) = make_float4(h[0][0], h[0][1], h[0][2], h[0][3]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fabsf(h[0][i]));
     }
   } else {
+    float4 sg[kQuantVec], su[kQuantVec];
+    int4 g[kQuantVec], u[kQuantVec];
+#pragma unroll
+    for (int j = 0; j < kQuantVec; ++j) {
+      const int v = min(t0 + j * stride, nvec - 1);
+      sg[j] = scales4(v * 4);
+      su[j] = scales4(p.inter + v * 4);
+    }
+    griddep_wait();
+#pragma unroll
+    for (int j = 0; j < kQuantVec; ++j) {
+      const int v = min(t0 + j * stride, nvec - 1);
+      g[j] = *reinterpret_cast<const int4*>(gu + v * 4);
+      u[j] = *reinterpret_cast<const int4*>(gu + p.inter + v * 4);
+    }
 #pragma unroll
     for (int j = 0; j < kQuantVec; ++j) {
       const int v = t0 + j * stride;
       if (v < nvec) {
-        row4(v * 4, h[j]);
+        add_slices(g[j], v * 4);
+        add_slices(u[j], p.inter + v * 4);
+        silu4(g[j], u[j], sg[j], su[j], h[j]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fabsf(h[j][i]));
       }
@@ -330,7 +362,7 @@ __global__ void __launch_bounds__(kQuantThreads) moe_quant_kernel(Args p) {
   }
   amax = quant::row_max<CLUSTER>(amax, red);
   const float scale = __fdiv_rn(fmaxf(amax, 1e-12f), 127.0f), inv = __fdiv_rn(1.0f, scale);
-  int8_t* q = p.q + static_cast<int64_t>(pos) * p.inter;
+  int8_t* q = p.q + static_cast<int64_t>(place) * p.inter;
   quant::Args qa = {};
   if constexpr (LONG) {
     for (int v = t0; v < nvec; v += stride) {
@@ -352,14 +384,13 @@ __global__ void __launch_bounds__(kQuantThreads) moe_quant_kernel(Args p) {
   if constexpr (CLUSTER) quant::cluster_arrive_wait_relaxed();  // peers may still read red[32]
 }
 
-// out[i][j .. j + 3]: the slots in order, four at a time.  The loads of all four
-// are issued before any is used, of slots without an expert too (their rows of
-// the workspace hold anything, and are not used): one slot after another, each
-// waiting for its own chain of loads, took 8 us for 6 slots of 4 tokens.
+// out[i][j .. j + 3]: the slots in order, eight at a time.  What does not come
+// from the down product is read before the wait (the kernels before it have
+// waited for whatever wrote it); the loads of all eight slots' sums are issued
+// before any is used, of slots without an expert too (their rows of the
+// workspace hold anything, and are not used).
 __global__ void __launch_bounds__(128) moe_combine_kernel(Args p) {
-  constexpr int S = 4;
-  griddep_wait();
-  griddep_launch_dependents();
+  constexpr int S = 8;
   const int i = blockIdx.y, j = (blockIdx.x * 128 + threadIdx.x) * 4;
   if (j >= p.hidden) return;
   const int64_t slice = static_cast<int64_t>(p.m) * p.topk * p.hidden;
@@ -372,20 +403,28 @@ __global__ void __launch_bounds__(128) moe_combine_kernel(Args p) {
     for (int s = 0; s < S; ++s) {
       const int pair = i * p.topk + min(s0 + s, p.topk - 1);
       rec[s] = __ldg(p.by_pair + pair);
-      acc[s] = __ldg(reinterpret_cast<const int4*>(p.part + static_cast<int64_t>(pair) * p.hidden + j));
       sh[s] = __ldg(p.sh + pair);
       wt[s] = __ldg(p.wt + pair);
     }
 #pragma unroll
     for (int s = 0; s < S; ++s)
       s2[s] = __ldg(reinterpret_cast<const float4*>(p.s2 + static_cast<int64_t>(max(rec[s].x, 0)) * p.hidden + j));
+    if (s0 == 0) {
+      griddep_wait();
+      griddep_launch_dependents();
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const int pair = i * p.topk + min(s0 + s, p.topk - 1);
+      acc[s] = *reinterpret_cast<const int4*>(p.part + static_cast<int64_t>(pair) * p.hidden + j);
+    }
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       if (s0 + s >= p.topk || rec[s].x < 0) continue;
       const int32_t* part = p.part + (static_cast<int64_t>(i) * p.topk + s0 + s) * p.hidden + j;
       const int n = stream::slices_of(rec[s].y + j / stream::kRows * rec[s].z, p.down.num_kb, rec[s].w);
       for (int k = 1; k < n; ++k) {
-        const int4 v = __ldg(reinterpret_cast<const int4*>(part + k * slice));
+        const int4 v = *reinterpret_cast<const int4*>(part + k * slice);
         acc[s].x += v.x;
         acc[s].y += v.y;
         acc[s].z += v.z;
@@ -427,6 +466,16 @@ inline cudaError_t launch_quant(const Args& a, int num_sms, cudaStream_t stream)
   return launch_pdl(moe_quant_kernel<false, false>, grid, block, 0, stream, 1, a);
 }
 
+inline cudaError_t carveout_once(void (*kernel)(Args), int dev, int slot) {
+  static std::atomic<unsigned long long> done[4] = {};
+  const unsigned long long bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0ull;
+  if (bit && (done[slot].load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                             cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess && bit) done[slot].fetch_or(bit, std::memory_order_acq_rel);
+  return e;
+}
+
 // Returns 0, 1 when a tensor map could not be made, 2 with *err set.
 inline int launch(const Args& a, const int8_t* x, const int8_t* w13, const int8_t* w2, int dev, int num_sms,
                   cudaStream_t stream, cudaError_t* err) {
@@ -440,6 +489,12 @@ inline int launch(const Args& a, const int8_t* x, const int8_t* w13, const int8_
   const size_t most = stream::kRingBytes + 1024;
   if ((*err = gemm::set_smem_once(moe_gate_up_kernel, dev, 0, most)) != cudaSuccess) return 2;
   if ((*err = gemm::set_smem_once(moe_down_kernel, dev, 1, most)) != cudaSuccess) return 2;
+  // An SM's split between L1 and shared memory does not change while a CTA runs on
+  // it: kernels 2 and 4 share SMs with 1 and 3 only under theirs.
+  if ((*err = carveout_once(moe_quant_kernel<true, true>, dev, 0)) != cudaSuccess) return 2;
+  if ((*err = carveout_once(moe_quant_kernel<true, false>, dev, 1)) != cudaSuccess) return 2;
+  if ((*err = carveout_once(moe_quant_kernel<false, false>, dev, 2)) != cudaSuccess) return 2;
+  if ((*err = carveout_once(moe_combine_kernel, dev, 3)) != cudaSuccess) return 2;
   *err = launch_pdl(moe_gate_up_kernel, dim3(a.up_grid), dim3(stream::kThreads), stream::smem_bytes(a.up), stream, 1,
                     tw13, tx, a);
   if (*err == cudaSuccess) *err = launch_quant(a, num_sms, stream);

@@ -745,21 +745,19 @@ qk_status qk_w8a8_lora_gemm(int m, int n, int k, const int8_t* a, const int8_t* 
   return cuda_status(lora::launch_expand(la, dev->sms, s), "adapter expand launch");
 }
 
-// ---- a MoE layer for a few tokens; the workspace holds the sorted pairs, the gate
+// ---- a MoE layer for a few tokens; the workspace holds the pairs' records, the gate
 // and up sums, the down sums, the scales of h and its int8 values
 namespace {
 constexpr int kMoeLayerTokens = 64, kMoeLayerTopk = 32, kMoeLayerExperts = moe::kMaxExperts;
 
 struct MoeLayout {
-  size_t by_pos, by_pair, gu, part, sh, q, total;  // byte offsets; by_pos is at 0
+  size_t gu, part, sh, q, total;  // byte offsets (the pairs' records are at 0)
 };
 
 MoeLayout moe_layout(const moe::Args& a) {
   const size_t pairs = static_cast<size_t>(a.m) * a.topk;
   MoeLayout l;
-  l.by_pos = 0;
-  l.by_pair = round256(pairs * 16);
-  l.gu = l.by_pair + round256(pairs * 16);
+  l.gu = round256(pairs * 16);
   l.part = l.gu + round256(pairs * a.inter * 8 * a.up.max_slices);
   l.sh = l.part + round256(pairs * a.hidden * 4 * a.down.max_slices);
   l.q = l.sh + round256(pairs * 4);
@@ -832,8 +830,7 @@ qk_status qk_w8a8_moe_layer(int m, int hidden, int inter, int num_experts, int t
   g.wt = topk_weights;
   g.s13 = scale_gate_up;
   g.s2 = scale_down;
-  g.by_pos = reinterpret_cast<int4*>(ws + l.by_pos);
-  g.by_pair = reinterpret_cast<int4*>(ws + l.by_pair);
+  g.by_pair = reinterpret_cast<int4*>(ws);
   g.gu = reinterpret_cast<int32_t*>(ws + l.gu);
   g.part = reinterpret_cast<int32_t*>(ws + l.part);
   g.sh = reinterpret_cast<float*>(ws + l.sh);
