@@ -161,7 +161,6 @@ def test_workspace_queries():
     for bad in ((0, 16, 32, 8), (4, 0, 32, 8), (4, 12, 32, 8), (4, 16, 40, 8), (4, 16, 32, 4), (4, 16, 32, 200),
                 (4, 16, 133152, 8)):
         assert qk.qk_w8a8_lora_gemm_workspace_size(*bad) == 0
-    assert qk.qk_w8a8_lora_gemm_workspace_size(4, 16, 32, 8) >= 4 * 8 * 4
     for bad in ((0, 32, 48, 3, 2), (65, 32, 48, 3, 2), (4, 40, 48, 3, 2), (4, 32, 24, 3, 2), (4, 32, 48, 0, 2),
                 (4, 32, 48, 3, 0), (4, 32, 48, 3, 33), (4, 32, 48, 1025, 2)):
         assert qk.qk_w8a8_moe_layer_workspace_size(*bad) == 0

@@ -661,18 +661,20 @@ size_t qk_w8a8_linear_workspace_size(int m, int n, int k, int group_k) {
          round256(static_cast<size_t>(m) * 4);
 }
 
-// ---- adapters beside the projection; the workspace holds the GEMM's own
-// part, then s [m, rank], then the int32 sums [m, n]
+// ---- adapters beside the projection; the workspace holds the GEMM's own part,
+// then s [parts, m, rank], then the int32 sums [slices, m, n]
 namespace {
 struct LoraLayout {
   size_t gemm, s, c, total;
 };
 
-LoraLayout lora_layout(int m, int n, int k, int rank) {
+LoraLayout lora_layout(int m, int n, int k, int rank, int num_sms) {
   LoraLayout l;
-  l.gemm = round256(qk_w8a8_gemm_workspace_size(m, n, k, 0));
-  l.s = round256(static_cast<size_t>(m) * rank * 4);
-  l.c = round256(static_cast<size_t>(m) * static_cast<size_t>(n) * 4);
+  const bool small = lora::streams(m);
+  l.gemm = small ? 0 : round256(qk_w8a8_gemm_workspace_size(m, n, k, 0));
+  l.s = round256(static_cast<size_t>(lora::shrink_parts(m, k, num_sms)) * m * rank * 4);
+  l.c = round256(static_cast<size_t>(small ? lora::stream_plan(m, n, k, num_sms).max_slices : 1) * m *
+                 static_cast<size_t>(n) * 4);
   l.total = l.gemm + l.s + l.c;
   return l;
 }
@@ -685,8 +687,9 @@ qk_status lora_check(int m, int n, int k, int rank) {
 }  // namespace
 
 size_t qk_w8a8_lora_gemm_workspace_size(int m, int n, int k, int rank) {
-  if (lora_check(m, n, k, rank) != QK_OK || m == 0 || n == 0) return 0;
-  return lora_layout(m, n, k, rank).total;
+  const DeviceInfo* dev = nullptr;
+  if (lora_check(m, n, k, rank) != QK_OK || m == 0 || n == 0 || check_device(&dev) != QK_OK) return 0;
+  return lora_layout(m, n, k, rank, dev->sms).total;
 }
 
 qk_status qk_w8a8_lora_gemm(int m, int n, int k, const int8_t* a, const int8_t* b, const float* scale_a,
@@ -710,7 +713,7 @@ qk_status qk_w8a8_lora_gemm(int m, int n, int k, const int8_t* a, const int8_t* 
   const DeviceInfo* dev = nullptr;
   st = check_device(&dev);
   if (st != QK_OK) return st;
-  const LoraLayout l = lora_layout(m, n, k, rank);
+  const LoraLayout l = lora_layout(m, n, k, rank, dev->sms);
   if (workspace == nullptr || workspace_bytes < l.total || !aligned(workspace, 256)) return QK_ERR_WORKSPACE;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
@@ -732,6 +735,10 @@ qk_status qk_w8a8_lora_gemm(int m, int n, int k, const int8_t* a, const int8_t* 
   la.c = reinterpret_cast<const int32_t*>(ws + l.gemm + l.s);
   la.out = out;
   la.out_bf16 = out_dtype == QK_BF16;
+  la.kparts = lora::shrink_parts(m, k, dev->sms);
+  la.kpart = ((k + la.kparts - 1) / la.kparts + 255) / 256 * 256;
+  int dev_id = 0;
+  cudaGetDevice(&dev_id);
   // the GEMM's counters and split-K accumulators start at zero
   gemm::PairPlan pl;
   if (l.gemm > 0 && pair_plan_for(m, n, k, 0, &pl) &&
@@ -739,8 +746,17 @@ qk_status qk_w8a8_lora_gemm(int m, int n, int k, const int8_t* a, const int8_t* 
     return QK_ERR_CUDA;
   st = cuda_status(lora::launch_shrink(la, x_dtype == QK_BF16, s), "adapter shrink launch");
   if (st != QK_OK) return st;
-  st = gemm_common(m, n, k, a, b, scale_a, scale_b, 0, output_scale, const_cast<int32_t*>(la.c), nullptr,
-                   out_dtype, l.gemm > 0 ? workspace : nullptr, l.gemm, stream, nullptr, nullptr);
+  if (lora::streams(m)) {
+    const stream::Plan sp = lora::stream_plan(m, n, k, dev->sms);
+    la.num_kb = sp.num_kb;
+    la.per = stream::share(sp.row_blocks, sp.num_kb, dev->sms);
+    cudaError_t e = cudaSuccess;
+    const int r = lora::launch_stream(la, a, b, sp, dev_id, dev->sms, s, &e);
+    st = r == 1 ? cuda_status(cudaErrorInvalidValue, "tensor map encoding") : cuda_status(e, "projection launch");
+  } else {
+    st = gemm_common(m, n, k, a, b, scale_a, scale_b, 0, output_scale, const_cast<int32_t*>(la.c), nullptr,
+                     out_dtype, l.gemm > 0 ? workspace : nullptr, l.gemm, stream, nullptr, nullptr);
+  }
   if (st != QK_OK) return st;
   return cuda_status(lora::launch_expand(la, dev->sms, s), "adapter expand launch");
 }
