@@ -2,18 +2,21 @@
 // projection: out = epilogue(a b^T) + s B[id]^T, s = lora_scale[id] * x A[id]^T,
 // where token i uses adapter id = ids[i] (none when outside [0, adapters)).
 //
-// Three kernels: s (the tokens into the adapters' ranks), the projection's
-// int32 sums (the stream of stream.cuh up to 64 tokens, the GEMM beyond), and
-// the output: the sums' epilogue plus s B^T, rounded once.
+// Three kernels: the projection's int32 sums, s (the tokens into the adapters'
+// ranks), and the output: the sums' epilogue plus s B^T, rounded once.  Up to 64
+// tokens the sums are the stream of stream.cuh, which runs first and leaves room
+// on its SMs: s is formed beside it (and waits for it at its end, so that the
+// last kernel, which waits for s, waits for both).  Beyond, the GEMM fills the
+// SMs, and s comes first.
 //
-// Both small products run on the bf16 matrix instruction, 16 tokens a tile.
+// Both small products run on the bf16 matrix instruction, 16 rows at a time.
 // A bf16 value is exact there; a binary32 one (s, and x when it is fp32) enters
 // as three bf16 terms, x = h + m + l, each the rounding of what is left: 24 bits,
-// so a product of 16 of them is as good as one of binary32 values.  Tokens of
-// a tile may use different adapters: each adapter present is multiplied with
-// the whole tile and the rows that use it take its result.  They take it by
-// selection, not by multiplying with zero, so that an adapter that holds NaN
-// or infinity reaches no row of another.
+// so a product of 16 of them is as good as one of binary32 values.  The 16 rows
+// are tokens of ONE adapter.  Up to 64 tokens they are gathered from the whole
+// batch, so an adapter is read once however its requests lie; in a longer batch,
+// where a request's tokens lie together, they come from 16 tokens in a row, an
+// adapter present there after another, with the other rows left out.
 #pragma once
 
 #include "qk_common.cuh"
@@ -39,9 +42,11 @@ struct Args {
   int num_kb, per;            // how c's tiles are cut into slices (per 0: not at all)
   void* out;
   int out_bf16;
+  int beside;                 // the sums are formed before s, and beside it
 };
 
-constexpr int kTile = 16;  // tokens of a tile
+constexpr int kTile = 16;     // rows of a group
+constexpr int kMaxParts = 8;  // K parts of s
 
 __device__ __forceinline__ int adapter_of(const Args& p, int row) {
   const int id = row < p.m ? __ldg(p.ids + row) : -1;
@@ -66,19 +71,94 @@ __device__ __forceinline__ void split3(float lo, float hi, uint32_t (&t)[3]) {
   }
 }
 
-// The tokens of tile `t` by adapter, by a whole warp: lane i < 16 holds token i's
-// adapter in `id`, -1 for none and -2 past the last token.  Returns a mask of the
-// lanes that show one first.
-__device__ __forceinline__ unsigned tile_groups(const Args& p, int t, int& id) {
+// Place of the n-th (from 0) set bit.
+__device__ __forceinline__ int nth_bit(unsigned mask, int n) {
+  for (; n > 0; --n) mask &= mask - 1u;
+  return __ffs(mask) - 1;
+}
+
+// 16 rows of one adapter (or of none: -1).
+struct Group {
+  int use;
+  int tok[kTile];  // -1: no token
+};
+
+// Unit `u` of a batch of up to 64 tokens: adapters in the order of their first
+// tokens, an adapter's tokens 16 to a unit.  By warp 0; false when there is none.
+// Without `none`, tokens without an adapter are passed over.
+__device__ __forceinline__ bool gather_unit(const Args& p, int u, bool none, Group& gr) {
+  const int lane = threadIdx.x & 31;
+  int id[2];
+  uint64_t same[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    id[h] = h * 32 + lane < p.m ? adapter_of(p, h * 32 + lane) : -2;
+    same[h] = static_cast<uint64_t>(__match_any_sync(0xFFFFFFFFu, id[h])) << (32 * h);
+  }
+#pragma unroll 8
+  for (int j = 0; j < 32; ++j) {
+    const int lo = __shfl_sync(0xFFFFFFFFu, id[0], j), hi = __shfl_sync(0xFFFFFFFFu, id[1], j);
+    if (id[1] == lo) same[1] |= 1ull << j;
+    if (id[0] == hi) same[0] |= 1ull << (32 + j);
+  }
+  int base = 0;
+  bool found = false;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const bool leads = id[h] >= (none ? -1 : 0) && (same[h] & ((1ull << (32 * h + lane)) - 1ull)) == 0;
+    const int units = leads ? (__popcll(same[h]) + kTile - 1) / kTile : 0;
+    int sum = units;  // inclusive prefix
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    const int at = base + sum - units;
+    const unsigned here = __ballot_sync(0xFFFFFFFFu, u >= at && u < at + units);
+    if (here != 0) {
+      const int src = __ffs(here) - 1;
+      uint64_t mask = __shfl_sync(0xFFFFFFFFu, same[h], src);
+      const int skip = (u - __shfl_sync(0xFFFFFFFFu, at, src)) * kTile + lane;
+      const int use = __shfl_sync(0xFFFFFFFFu, id[h], src);
+      if (lane == 0) gr.use = use;
+      if (lane < kTile) {
+        for (int n = 0; n < skip && mask != 0; ++n) mask &= mask - 1ull;
+        gr.tok[lane] = mask != 0 ? __ffsll(static_cast<long long>(mask)) - 1 : -1;
+      }
+      found = true;
+    }
+    base += __shfl_sync(0xFFFFFFFFu, sum, 31);
+  }
+  return found;
+}
+
+// The n-th adapter (or none) among tokens 16 t .. 16 t + 15, by warp 0.
+__device__ __forceinline__ bool tile_group(const Args& p, int t, int n, bool none, Group& gr) {
   const int lane = threadIdx.x & 31, row = t * kTile + lane;
-  id = (lane < kTile && row < p.m) ? adapter_of(p, row) : -2;
+  const int id = (lane < kTile && row < p.m) ? adapter_of(p, row) : -2;
   const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
-  return __ballot_sync(0xFFFFFFFFu, id >= -1 && (same & ((1u << lane) - 1u)) == 0);
+  const unsigned firsts =
+      __ballot_sync(0xFFFFFFFFu, id >= (none ? -1 : 0) && (same & ((1u << lane) - 1u)) == 0);
+  if (n >= __popc(firsts)) return false;
+  const int use = __shfl_sync(0xFFFFFFFFu, id, nth_bit(firsts, n));
+  if (lane == 0) gr.use = use;
+  if (lane < kTile) gr.tok[lane] = id == use ? row : -1;
+  return true;
+}
+
+// Group n of the CTA, by all threads; false after the last.
+__device__ __forceinline__ bool next_group(const Args& p, int n, bool none, Group& gr, int& ok) {
+  if (threadIdx.x < 32) {
+    const bool found = p.beside ? (n == 0 && gather_unit(p, blockIdx.x, none, gr))
+                                : tile_group(p, blockIdx.x, n, none, gr);
+    if (threadIdx.x == 0) ok = found ? 1 : 0;
+  }
+  __syncthreads();
+  return ok != 0;
 }
 
 // ---------------------------------------------------------------------------
-// s: one CTA per (token tile, adapter in it, K part and 64 ranks); its 8 warps
-// deal the part's K in steps of 32 and each multiplies all ranks.  The operands
+// s: one CTA per (group, K part and 64 ranks); its 8 warps deal the part's K in steps of 32 and each multiplies all ranks.  The operands
 // come straight from memory: a dot product may sum K in any order, so thread
 // (g, q) takes elements 8 q .. 8 q + 7 of a step (16 bytes) of token g, of token
 // g + 8 and of the adapter's row, four of them for each of two instructions, in
@@ -88,67 +168,84 @@ constexpr int kShrinkThreads = 256;
 constexpr int kShrinkStep = 32;
 constexpr int kMaxRank = 128, kRankGroup = 64;
 
-// Elements at .. at + 7 of x, as terms of four pairs.
+// Elements at .. at + 7 of x, and their four pairs as bf16 terms.
 template <bool BF16>
-__device__ __forceinline__ void load_x(const void* x, int64_t at, bool in, uint32_t (&v)[4][BF16 ? 1 : 3]) {
+__device__ __forceinline__ void load_x(const void* x, int64_t at, bool in, uint4 (&v)[BF16 ? 1 : 2]) {
+  const char* p = static_cast<const char*>(x) + at * (BF16 ? 2 : 4);
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 1 : 2); ++i)
+    v[i] = in ? ld_nc_v4(p + i * 16) : make_uint4(0, 0, 0, 0);
+}
+template <bool BF16>
+__device__ __forceinline__ void terms_x(const uint4 (&v)[BF16 ? 1 : 2], uint32_t (&t)[4][BF16 ? 1 : 3]) {
   if constexpr (BF16) {
-    const uint4 w = in ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x) + at))
-                       : make_uint4(0, 0, 0, 0);
-    v[0][0] = w.x;
-    v[1][0] = w.y;
-    v[2][0] = w.z;
-    v[3][0] = w.w;
+    t[0][0] = v[0].x;
+    t[1][0] = v[0].y;
+    t[2][0] = v[0].z;
+    t[3][0] = v[0].w;
   } else {
-    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
-    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const float4 a = in ? __ldg(f) : zero, b = in ? __ldg(f + 1) : zero;
-    split3(a.x, a.y, v[0]);
-    split3(a.z, a.w, v[1]);
-    split3(b.x, b.y, v[2]);
-    split3(b.z, b.w, v[3]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      split3(__uint_as_float(v[i].x), __uint_as_float(v[i].y), t[2 * i]);
+      split3(__uint_as_float(v[i].z), __uint_as_float(v[i].w), t[2 * i + 1]);
+    }
   }
 }
 
 template <bool BF16, int RT>  // RT: tiles of 8 ranks
-__global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(Args p) {
-  constexpr int NW = kShrinkThreads / 32, TERMS = BF16 ? 1 : 3;
+__global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_kernel(Args p) {
+  constexpr int NW = kShrinkThreads / 32, TERMS = BF16 ? 1 : 3, XV = BF16 ? 1 : 2;
   __shared__ float red[NW][kTile][RT * 8 + 1];
-  griddep_wait();
+  __shared__ Group gr;
+  __shared__ int ok;
+  // (beside the sums: x, the adapters and ids are the caller's, complete before the
+  // kernel of the sums let this one start, and s is free)
+  if (!p.beside) griddep_wait();
   griddep_launch_dependents();
-  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
-  int id;
-  const unsigned firsts = tile_groups(p, t, id) & __ballot_sync(0xFFFFFFFFu, id >= 0);
-  if (static_cast<int>(blockIdx.y) >= __popc(firsts)) return;
-  const int use = __shfl_sync(0xFFFFFFFFu, id, __fns(firsts, 0, blockIdx.y + 1));
-  const unsigned mine = __ballot_sync(0xFFFFFFFFu, id == use);  // tokens of this adapter
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  if (!next_group(p, blockIdx.y, false, gr, ok)) {
+    if (p.beside) griddep_wait();
+    return;
+  }
+  const int use = gr.use, tok0 = gr.tok[g], tok1 = gr.tok[g + 8];
   const int z = blockIdx.z % p.kparts, rg = blockIdx.z / p.kparts * kRankGroup, ranks = min(p.rank - rg, kRankGroup);
-  const int k0 = z * p.kpart, k1 = min(p.k, k0 + p.kpart), r0 = t * kTile;
+  const int k0 = z * p.kpart, k1 = min(p.k, k0 + p.kpart);
   const __nv_bfloat16* a = p.la + (static_cast<int64_t>(use) * p.rank + rg) * p.k;
   float acc[RT][4];
 #pragma unroll
   for (int j = 0; j < RT; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-  const bool in0 = (mine >> g) & 1u, in1 = (mine >> (g + 8)) & 1u;
-#pragma unroll(RT <= 2 ? 4 : (RT <= 4 ? 2 : 1))
-  for (int k = k0 + warp * kShrinkStep + q * 8; k < k1 + q * 8; k += NW * kShrinkStep) {
-    const bool in = k < k1;  // (K is a multiple of 16: the last step may be half one)
-    uint32_t x0[4][TERMS], x1[4][TERMS];
-    uint4 b[RT];
-    load_x<BF16>(p.x, static_cast<int64_t>(r0 + g) * p.k + k, in0 && in, x0);
-    load_x<BF16>(p.x, static_cast<int64_t>(r0 + g + 8) * p.k + k, in1 && in, x1);
+  // U steps' loads are issued together (ld_nc_v4 and mma_bf16 are volatile: they
+  // keep their order)
+  constexpr int U = RT <= 2 ? 4 : ((RT <= 4 || BF16) ? 2 : 1), ROW = NW * kShrinkStep;
+  for (int k = k0 + warp * kShrinkStep + q * 8; k < k1 + q * 8; k += U * ROW) {
+    uint4 x0[U][XV], x1[U][XV], b[U][RT];
 #pragma unroll
-    for (int j = 0; j < RT; ++j)
-      b[j] = (j * 8 < ranks && in) ? __ldg(reinterpret_cast<const uint4*>(a + static_cast<int64_t>(j * 8 + g) * p.k + k))
-                                   : make_uint4(0, 0, 0, 0);
+    for (int u = 0; u < U; ++u) {
+      const int ku = k + u * ROW;
+      const bool in = ku < k1;  // (K is a multiple of 16: the last step may be half one)
+      load_x<BF16>(p.x, static_cast<int64_t>(tok0) * p.k + ku, tok0 >= 0 && in, x0[u]);
+      load_x<BF16>(p.x, static_cast<int64_t>(tok1) * p.k + ku, tok1 >= 0 && in, x1[u]);
 #pragma unroll
-    for (int i = 0; i < TERMS; ++i) {
-      const uint32_t f0[4] = {x0[0][i], x1[0][i], x0[1][i], x1[1][i]};
-      const uint32_t f1[4] = {x0[2][i], x1[2][i], x0[3][i], x1[3][i]};
+      for (int j = 0; j < RT; ++j)
+        b[u][j] = (j * 8 < ranks && in) ? ld_nc_v4(a + static_cast<int64_t>(j * 8 + g) * p.k + ku)
+                                        : make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
-      for (int j = 0; j < RT; ++j) {
-        mma_bf16(acc[j], f0, b[j].x, b[j].y);
-        mma_bf16(acc[j], f1, b[j].z, b[j].w);
+    for (int u = 0; u < U; ++u) {
+      uint32_t t0[4][TERMS], t1[4][TERMS];
+      terms_x<BF16>(x0[u], t0);
+      terms_x<BF16>(x1[u], t1);
+#pragma unroll
+      for (int i = 0; i < TERMS; ++i) {
+        const uint32_t f0[4] = {t0[0][i], t1[0][i], t0[1][i], t1[1][i]};
+        const uint32_t f1[4] = {t0[2][i], t1[2][i], t0[3][i], t1[3][i]};
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+          mma_bf16(acc[j], f0, b[u][j].x, b[u][j].y);
+          mma_bf16(acc[j], f1, b[u][j].z, b[u][j].w);
+        }
       }
     }
   }
@@ -164,124 +261,145 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(Args p) {
   float* s = p.s + static_cast<int64_t>(z) * p.m * p.rank + rg;
   for (int i = tid; i < kTile * ranks; i += kShrinkThreads) {
     const int row = i / ranks, r = i - row * ranks;
-    if (!((mine >> row) & 1u)) continue;
+    if (gr.tok[row] < 0) continue;
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) v += red[w][row][r];
-    s[static_cast<int64_t>(r0 + row) * p.rank + r] = ls * v;
+    s[static_cast<int64_t>(gr.tok[row]) * p.rank + r] = ls * v;
   }
+  if (p.beside) griddep_wait();
 }
 
 // ---------------------------------------------------------------------------
-// out: a CTA takes 16 tokens by 256 columns, a warp 32 of the columns, and one
-// group of tokens after another (those of an adapter, or of none); where the
-// grid would be small the groups go to CTAs of their own.  Column 2 q + b of the
-// j-th product of a warp stands for column 8 q + 2 j + b of its 32, so that a
-// thread ends up with 8 consecutive columns of rows g and g + 8: 16-byte reads of
-// the sums, 16-byte writes.  All but the sums is read, and multiplied, before
-// the wait for the projection: it is the caller's, or the kernel's before that.
+// out: a CTA takes the 16 rows of a group (or one group of a tile after another)
+// by 256 columns, a warp 32 of the columns.  Column 2 q + b of the j-th product of
+// a warp stands for column 8 q + 2 j + b of its 32, so that a thread ends up with
+// 8 consecutive columns of rows g and g + 8: 16-byte reads of the sums, 16-byte
+// writes.  The adapter's rows are requested first (before the wait, which a CTA
+// that starts early spends on them: they are the caller's), then the sums' slices
+// and s.
 // ---------------------------------------------------------------------------
 constexpr int kExpandThreads = 256;
 constexpr int kExpandCols = 256;
 
-inline size_t expand_smem(int rank) { return static_cast<size_t>(3) * kTile * ((rank + 15) / 16 * 8 + 4) * 4; }
+inline size_t expand_smem(int rank) { return static_cast<size_t>(3) * kTile * ((rank + 31) / 32 * 16 + 4) * 4; }
 
-__global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(Args p) {
-  extern __shared__ uint32_t ss[];  // s: [term][token][rank / 2 words], rows padded by 16 bytes
-  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
-  const int r0 = t * kTile, steps = (p.rank + 15) / 16, pitch = steps * 8 + 4;
+__global__ void __launch_bounds__(kExpandThreads, 3) lora_expand_kernel(Args p) {
+  extern __shared__ uint32_t ss[];  // s: [term][row][rank / 2 words], rows padded by 16 bytes
+  __shared__ Group gr;
+  __shared__ int ok;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  const int steps = (p.rank + 31) / 32, pitch = steps * 16 + 4;
   const int col0 = blockIdx.y * kExpandCols + warp * 32, col = col0 + q * 8;
   const bool in = col < p.n;  // (n is a multiple of 8)
-  bool waited = false;
-  int id;
-  const unsigned firsts = tile_groups(p, t, id);
-  const int groups = __popc(firsts);
-  const int id0 = __shfl_sync(0xFFFFFFFFu, id, g), id1 = __shfl_sync(0xFFFFFFFFu, id, g + 8);
-  const float sa0 = id0 >= -1 ? __ldg(p.sa + r0 + g) : 0.0f, sa1 = id1 >= -1 ? __ldg(p.sa + r0 + g + 8) : 0.0f;
   const int slices = (in && p.per > 0) ? stream::slices_of(col / stream::kRows, p.num_kb, p.per) : 1;
-  float4 sw[2] = {};
-  if (in) {
-    sw[0] = __ldg(reinterpret_cast<const float4*>(p.sw + col));
-    sw[1] = __ldg(reinterpret_cast<const float4*>(p.sw + col) + 1);
-  }
-  for (int n = blockIdx.z; n < groups; n += gridDim.z) {
-    const int use = __shfl_sync(0xFFFFFFFFu, id, __fns(firsts, 0, n + 1));
-    const unsigned mine = __ballot_sync(0xFFFFFFFFu, id == use);
+  const int64_t slice = static_cast<int64_t>(p.m) * p.n;
+  bool waited = false;
+  for (int n = blockIdx.z; next_group(p, n, true, gr, ok); n += gridDim.z) {
+    const int use = gr.use;
+    const __nv_bfloat16* b = p.lb + static_cast<int64_t>(use) * p.n * p.rank;
+    uint4 bv[4];
+    auto request = [&](int st) {  // 32 ranks of the adapter's rows
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = st * 32 + q * 8, c = col0 + (g >> 1) * 8 + j * 2 + (g & 1);
+        bv[j] = (c < p.n && r < p.rank) ? ld_nc_v4(b + static_cast<int64_t>(c) * p.rank + r) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    if (use >= 0) request(0);
+    if (!waited) {
+      griddep_wait();
+      griddep_launch_dependents();
+      waited = true;
+    }
+    int4 c0[2], c1[2];  // the sums of rows g and g + 8
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int tok = gr.tok[g + h * 8];
+      if (tok < 0 || !in) continue;
+      const int32_t* c = p.c + static_cast<int64_t>(tok) * p.n + col;
+      int4 e0[3], e1[3];
+      c0[h] = *reinterpret_cast<const int4*>(c);
+      c1[h] = *reinterpret_cast<const int4*>(c + 4);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const bool on = i + 1 < slices;
+        e0[i] = on ? *reinterpret_cast<const int4*>(c + (i + 1) * slice) : make_int4(0, 0, 0, 0);
+        e1[i] = on ? *reinterpret_cast<const int4*>(c + (i + 1) * slice + 4) : make_int4(0, 0, 0, 0);
+      }
+      auto add = [](int4& x, const int4& y) { x = make_int4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w); };
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        add(c0[h], e0[i]);
+        add(c1[h], e1[i]);
+      }
+      for (int i = 4; i < slices; ++i) {
+        add(c0[h], *reinterpret_cast<const int4*>(c + i * slice));
+        add(c1[h], *reinterpret_cast<const int4*>(c + i * slice + 4));
+      }
+    }
     float d[4][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) d[j][i] = 0.0f;
     if (use >= 0) {
-      for (int i = tid; i < kTile * steps * 8; i += kExpandThreads) {
-        const int row = i / (steps * 8), w = i - row * (steps * 8), r = 2 * w;
-        if (!((mine >> row) & 1u)) continue;
-        float lo = 0.0f, hi = 0.0f;
-        if (r < p.rank) {
-          const float* s = p.s + static_cast<int64_t>(r0 + row) * p.rank + r;
-#pragma unroll 4
-          for (int z = 0; z < p.kparts; ++z) {
-            const float2 f = *reinterpret_cast<const float2*>(s + static_cast<int64_t>(z) * p.m * p.rank);
-            lo += f.x;
-            hi += f.y;
+      for (int i = tid; i < kTile * steps * 16; i += kExpandThreads) {
+        const int row = i / (steps * 16), w = i - row * (steps * 16), r = 2 * w, tok = gr.tok[row];
+        uint32_t term[3] = {0, 0, 0};
+        if (tok >= 0 && r < p.rank) {
+          const float* s = p.s + static_cast<int64_t>(tok) * p.rank + r;
+          float2 f[kMaxParts];
+#pragma unroll
+          for (int z = 0; z < kMaxParts; ++z)
+            f[z] = z < p.kparts ? *reinterpret_cast<const float2*>(s + static_cast<int64_t>(z) * p.m * p.rank)
+                                : make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int z = 1; z < kMaxParts; ++z) {
+            f[0].x += f[z].x;
+            f[0].y += f[z].y;
           }
+          split3(f[0].x, f[0].y, term);
         }
-        uint32_t term[3];
-        split3(lo, hi, term);
 #pragma unroll
         for (int e = 0; e < 3; ++e) ss[(e * kTile + row) * pitch + w] = term[e];
       }
       __syncthreads();
-      const __nv_bfloat16* b = p.lb + static_cast<int64_t>(use) * p.n * p.rank;
-      const bool in0 = id0 == use, in1 = id1 == use;
-#pragma unroll 2
       for (int st = 0; st < steps; ++st) {
-        const int r = st * 16 + q * 4;
-        uint2 bv[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int c = col0 + (g >> 1) * 8 + j * 2 + (g & 1);
-          bv[j] = (c < p.n && r < p.rank)
-                      ? __ldg(reinterpret_cast<const uint2*>(b + static_cast<int64_t>(c) * p.rank + r))
-                      : make_uint2(0, 0);
-        }
+        if (st > 0) request(st);
+        const int at = st * 16 + q * 4;
 #pragma unroll
         for (int e = 0; e < 3; ++e) {
-          // (rows of other groups were not written: they must not be read as numbers)
-          const uint2 zero = make_uint2(0, 0);
-          const uint2 x0 = in0 ? *reinterpret_cast<const uint2*>(&ss[(e * kTile + g) * pitch + st * 8 + q * 2]) : zero;
-          const uint2 x1 = in1 ? *reinterpret_cast<const uint2*>(&ss[(e * kTile + g + 8) * pitch + st * 8 + q * 2]) : zero;
-          const uint32_t f[4] = {x0.x, x1.x, x0.y, x1.y};
+          const uint4 x0 = *reinterpret_cast<const uint4*>(&ss[(e * kTile + g) * pitch + at]);
+          const uint4 x1 = *reinterpret_cast<const uint4*>(&ss[(e * kTile + g + 8) * pitch + at]);
+          const uint32_t f0[4] = {x0.x, x1.x, x0.y, x1.y}, f1[4] = {x0.z, x1.z, x0.w, x1.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mma_bf16(d[j], f, bv[j].x, bv[j].y);
+          for (int j = 0; j < 4; ++j) {
+            mma_bf16(d[j], f0, bv[j].x, bv[j].y);
+            mma_bf16(d[j], f1, bv[j].z, bv[j].w);
+          }
         }
       }
     }
-    if (!waited) {
-      griddep_wait();
-      griddep_launch_dependents();
-      waited = true;
+    float4 sw[2] = {};
+    if (in) {
+      sw[0] = __ldg(reinterpret_cast<const float4*>(p.sw + col));
+      sw[1] = __ldg(reinterpret_cast<const float4*>(p.sw + col) + 1);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if ((h ? id1 : id0) != use || !in) continue;
-      const int64_t o = static_cast<int64_t>(r0 + g + h * 8) * p.n + col;
-      int4 c0 = *reinterpret_cast<const int4*>(p.c + o), c1 = *reinterpret_cast<const int4*>(p.c + o + 4);
-      for (int i = 1; i < slices; ++i) {
-        const int32_t* c = p.c + static_cast<int64_t>(i) * p.m * p.n + o;
-        const int4 e0 = *reinterpret_cast<const int4*>(c), e1 = *reinterpret_cast<const int4*>(c + 4);
-        c0 = make_int4(c0.x + e0.x, c0.y + e0.y, c0.z + e0.z, c0.w + e0.w);
-        c1 = make_int4(c1.x + e1.x, c1.y + e1.y, c1.z + e1.z, c1.w + e1.w);
-      }
-      const float sa = h ? sa1 : sa0;
+      const int tok = gr.tok[g + h * 8];
+      if (tok < 0 || !in) continue;
+      const int64_t o = static_cast<int64_t>(tok) * p.n + col;
+      const float sa = __ldg(p.sa + tok);
       auto val = [&](int acc, float s, float add) {
         const float v = __fmul_rn(__fmul_rn(__fmul_rn(__int2float_rn(acc), sa), s), p.alpha);
         return use >= 0 ? __fadd_rn(v, add) : v;
       };
-      const float v0 = val(c0.x, sw[0].x, d[0][2 * h]), v1 = val(c0.y, sw[0].y, d[0][2 * h + 1]);
-      const float v2 = val(c0.z, sw[0].z, d[1][2 * h]), v3 = val(c0.w, sw[0].w, d[1][2 * h + 1]);
-      const float v4 = val(c1.x, sw[1].x, d[2][2 * h]), v5 = val(c1.y, sw[1].y, d[2][2 * h + 1]);
-      const float v6 = val(c1.z, sw[1].z, d[3][2 * h]), v7 = val(c1.w, sw[1].w, d[3][2 * h + 1]);
+      const float v0 = val(c0[h].x, sw[0].x, d[0][2 * h]), v1 = val(c0[h].y, sw[0].y, d[0][2 * h + 1]);
+      const float v2 = val(c0[h].z, sw[0].z, d[1][2 * h]), v3 = val(c0[h].w, sw[0].w, d[1][2 * h + 1]);
+      const float v4 = val(c1[h].x, sw[1].x, d[2][2 * h]), v5 = val(c1[h].y, sw[1].y, d[2][2 * h + 1]);
+      const float v6 = val(c1[h].z, sw[1].z, d[3][2 * h]), v7 = val(c1[h].w, sw[1].w, d[3][2 * h + 1]);
       if (p.out_bf16) {
         *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + o) =
             make_uint4(pack_bf16x2(v0, v1), pack_bf16x2(v2, v3), pack_bf16x2(v4, v5), pack_bf16x2(v6, v7));
@@ -291,12 +409,9 @@ __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(Args p) {
         out[1] = make_float4(v4, v5, v6, v7);
       }
     }
-    if (n + gridDim.z < groups) __syncthreads();  // s is rewritten
+    __syncthreads();  // the group and s are rewritten
   }
-  if (!waited) {
-    griddep_wait();
-    griddep_launch_dependents();
-  }
+  if (!waited) griddep_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -336,30 +451,47 @@ __global__ void __launch_bounds__(stream::kThreads, 1)
 
 inline bool streams(int m) { return m <= stream::kMaxTokens; }
 
-inline stream::Plan stream_plan(int m, int n, int k, int num_sms) { return stream::plan(m, n, k, num_sms); }
+// (a ring of 172 KB leaves room for a CTA of s, with its 33 KB for 64 ranks)
+constexpr size_t kRing = 172 * 1024;
+inline stream::Plan stream_plan(int m, int n, int k, int num_sms) { return stream::plan(m, n, k, num_sms, kRing); }
 
-// K parts of s: as many as keep its CTAs, one group a tile, within two an SM, no
-// part under 256 (one step of each warp).
-inline int shrink_parts(int m, int k, int num_sms) {
-  const int tiles = (m + kTile - 1) / kTile, most = m < 4 ? m : 4;
+// Groups at most: of the whole batch (gathered; a token without an adapter is in
+// none or, for the output, in one more), or of a tile.
+inline int most_groups(int m, int adapters, bool none) {
+  const int a = adapters + (none ? 1 : 0);
+  if (streams(m)) return (a < m ? a : m) + m / kTile;
+  return a < kTile ? a : kTile;
+}
+
+// K parts of s: as many as keep its CTAs (in a long batch a tile's one or two
+// groups) within one an SM, no part under 512.  `adapters` 1 gives the most parts.
+inline int shrink_parts(int m, int k, int adapters, int num_sms) {
+  const int ctas = streams(m) ? most_groups(m, adapters, false) : (m + kTile - 1) / kTile * 2;
   int parts = 1;
-  while (parts < 16 && 2 * tiles * most * parts <= 2 * num_sms && k / (2 * parts) >= 256) parts *= 2;
+  while (parts < kMaxParts && 2 * ctas * parts <= num_sms && k / (2 * parts) >= 512) parts *= 2;
   return parts;
 }
 
-template <bool BF16>
-inline cudaError_t launch_shrink_t(const Args& a, cudaStream_t stream) {
-  const int most = a.m < kTile ? a.m : kTile;
-  const int groups = (a.rank + kRankGroup - 1) / kRankGroup;
-  const dim3 grid((a.m + kTile - 1) / kTile, a.adapters < most ? a.adapters : most, a.kparts * groups);
-  const dim3 block(kShrinkThreads);
-  if (a.rank <= 16) return launch_pdl(lora_shrink_kernel<BF16, 2>, grid, block, 0, stream, 1, a);
-  if (a.rank <= 32) return launch_pdl(lora_shrink_kernel<BF16, 4>, grid, block, 0, stream, 1, a);
-  return launch_pdl(lora_shrink_kernel<BF16, 8>, grid, block, 0, stream, 1, a);
+template <bool BF16, int RT>
+inline cudaError_t launch_shrink_rt(const Args& a, dim3 grid, int dev, cudaStream_t stream) {
+  if (a.beside) {
+    const cudaError_t e = stream::shares_sm_once(lora_shrink_kernel<BF16, RT>, dev, (BF16 ? 8 : 0) + RT / 4);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(lora_shrink_kernel<BF16, RT>, grid, dim3(kShrinkThreads), 0, stream, 1, a);
 }
 
-inline cudaError_t launch_shrink(const Args& a, bool x_bf16, cudaStream_t stream) {
-  return x_bf16 ? launch_shrink_t<true>(a, stream) : launch_shrink_t<false>(a, stream);
+template <bool BF16>
+inline cudaError_t launch_shrink_t(const Args& a, int dev, cudaStream_t stream) {
+  const int most = most_groups(a.m, a.adapters, false), rgroups = (a.rank + kRankGroup - 1) / kRankGroup;
+  const dim3 grid(a.beside ? most : (a.m + kTile - 1) / kTile, a.beside ? 1 : most, a.kparts * rgroups);
+  if (a.rank <= 16) return launch_shrink_rt<BF16, 2>(a, grid, dev, stream);
+  if (a.rank <= 32) return launch_shrink_rt<BF16, 4>(a, grid, dev, stream);
+  return launch_shrink_rt<BF16, 8>(a, grid, dev, stream);
+}
+
+inline cudaError_t launch_shrink(const Args& a, bool x_bf16, int dev, cudaStream_t stream) {
+  return x_bf16 ? launch_shrink_t<true>(a, dev, stream) : launch_shrink_t<false>(a, dev, stream);
 }
 
 // Returns 0, 1 when a tensor map could not be made, 2 with *err set.
@@ -373,15 +505,15 @@ inline int launch_stream(const Args& a, const int8_t* x, const int8_t* w, const 
   return *err == cudaSuccess ? 0 : 2;
 }
 
-// Groups a tile can have go to CTAs of their own while the grid stays within
-// sixteen CTAs an SM.
+// A long batch's tiles take their groups one after another, unless the grid is
+// small enough for CTAs of their own (sixteen an SM).
 inline cudaError_t launch_expand(const Args& a, int num_sms, cudaStream_t stream) {
-  const int64_t tiles = (a.m + kTile - 1) / kTile, cols = (a.n + kExpandCols - 1) / kExpandCols;
-  const int most = a.m < kTile ? a.m : kTile, groups = a.adapters < most ? a.adapters + 1 : most;
-  int64_t z = 16LL * num_sms / (tiles * cols);
-  z = z < 1 ? 1 : (z > groups ? groups : z);
-  return launch_pdl(lora_expand_kernel, dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(cols), static_cast<unsigned>(z)),
-                    dim3(kExpandThreads), expand_smem(a.rank), stream, 1, a);
+  const int most = most_groups(a.m, a.adapters, true);
+  const int64_t tiles = a.beside ? most : (a.m + kTile - 1) / kTile, cols = (a.n + kExpandCols - 1) / kExpandCols;
+  int64_t z = a.beside ? 1 : 16LL * num_sms / (tiles * cols);
+  z = z < 1 ? 1 : (z > most ? most : z);
+  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(cols), static_cast<unsigned>(z));
+  return launch_pdl(lora_expand_kernel, grid, dim3(kExpandThreads), expand_smem(a.rank), stream, 1, a);
 }
 
 }  // namespace lora

@@ -466,16 +466,6 @@ inline cudaError_t launch_quant(const Args& a, int num_sms, cudaStream_t stream)
   return launch_pdl(moe_quant_kernel<false, false>, grid, block, 0, stream, 1, a);
 }
 
-inline cudaError_t carveout_once(void (*kernel)(Args), int dev, int slot) {
-  static std::atomic<unsigned long long> done[4] = {};
-  const unsigned long long bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0ull;
-  if (bit && (done[slot].load(std::memory_order_acquire) & bit)) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                             cudaSharedmemCarveoutMaxShared);
-  if (e == cudaSuccess && bit) done[slot].fetch_or(bit, std::memory_order_acq_rel);
-  return e;
-}
-
 // Returns 0, 1 when a tensor map could not be made, 2 with *err set.
 inline int launch(const Args& a, const int8_t* x, const int8_t* w13, const int8_t* w2, int dev, int num_sms,
                   cudaStream_t stream, cudaError_t* err) {
@@ -489,12 +479,10 @@ inline int launch(const Args& a, const int8_t* x, const int8_t* w13, const int8_
   const size_t most = stream::kRingBytes + 1024;
   if ((*err = gemm::set_smem_once(moe_gate_up_kernel, dev, 0, most)) != cudaSuccess) return 2;
   if ((*err = gemm::set_smem_once(moe_down_kernel, dev, 1, most)) != cudaSuccess) return 2;
-  // An SM's split between L1 and shared memory does not change while a CTA runs on
-  // it: kernels 2 and 4 share SMs with 1 and 3 only under theirs.
-  if ((*err = carveout_once(moe_quant_kernel<true, true>, dev, 0)) != cudaSuccess) return 2;
-  if ((*err = carveout_once(moe_quant_kernel<true, false>, dev, 1)) != cudaSuccess) return 2;
-  if ((*err = carveout_once(moe_quant_kernel<false, false>, dev, 2)) != cudaSuccess) return 2;
-  if ((*err = carveout_once(moe_combine_kernel, dev, 3)) != cudaSuccess) return 2;
+  if ((*err = stream::shares_sm_once(moe_quant_kernel<true, true>, dev, 0)) != cudaSuccess) return 2;
+  if ((*err = stream::shares_sm_once(moe_quant_kernel<true, false>, dev, 1)) != cudaSuccess) return 2;
+  if ((*err = stream::shares_sm_once(moe_quant_kernel<false, false>, dev, 2)) != cudaSuccess) return 2;
+  if ((*err = stream::shares_sm_once(moe_combine_kernel, dev, 3)) != cudaSuccess) return 2;
   *err = launch_pdl(moe_gate_up_kernel, dim3(a.up_grid), dim3(stream::kThreads), stream::smem_bytes(a.up), stream, 1,
                     tw13, tx, a);
   if (*err == cudaSuccess) *err = launch_quant(a, num_sms, stream);

@@ -672,7 +672,7 @@ LoraLayout lora_layout(int m, int n, int k, int rank, int num_sms) {
   LoraLayout l;
   const bool small = lora::streams(m);
   l.gemm = small ? 0 : round256(qk_w8a8_gemm_workspace_size(m, n, k, 0));
-  l.s = round256(static_cast<size_t>(lora::shrink_parts(m, k, num_sms)) * m * rank * 4);
+  l.s = round256(static_cast<size_t>(lora::shrink_parts(m, k, 1, num_sms)) * m * rank * 4);
   l.c = round256(static_cast<size_t>(small ? lora::stream_plan(m, n, k, num_sms).max_slices : 1) * m *
                  static_cast<size_t>(n) * 4);
   l.total = l.gemm + l.s + l.c;
@@ -735,25 +735,28 @@ qk_status qk_w8a8_lora_gemm(int m, int n, int k, const int8_t* a, const int8_t* 
   la.c = reinterpret_cast<const int32_t*>(ws + l.gemm + l.s);
   la.out = out;
   la.out_bf16 = out_dtype == QK_BF16;
-  la.kparts = lora::shrink_parts(m, k, dev->sms);
+  la.kparts = lora::shrink_parts(m, k, num_adapters, dev->sms);
   la.kpart = ((k + la.kparts - 1) / la.kparts + 255) / 256 * 256;
   int dev_id = 0;
   cudaGetDevice(&dev_id);
-  // the GEMM's counters and split-K accumulators start at zero
-  gemm::PairPlan pl;
-  if (l.gemm > 0 && pair_plan_for(m, n, k, 0, &pl) &&
-      cudaMemsetAsync(workspace, 0, gemm::pair_workspace_zero_bytes(pl), s) != cudaSuccess)
-    return QK_ERR_CUDA;
-  st = cuda_status(lora::launch_shrink(la, x_dtype == QK_BF16, s), "adapter shrink launch");
-  if (st != QK_OK) return st;
-  if (lora::streams(m)) {
+  la.beside = lora::streams(m) ? 1 : 0;
+  if (la.beside) {
     const stream::Plan sp = lora::stream_plan(m, n, k, dev->sms);
     la.num_kb = sp.num_kb;
     la.per = stream::share(sp.row_blocks, sp.num_kb, dev->sms);
     cudaError_t e = cudaSuccess;
     const int r = lora::launch_stream(la, a, b, sp, dev_id, dev->sms, s, &e);
     st = r == 1 ? cuda_status(cudaErrorInvalidValue, "tensor map encoding") : cuda_status(e, "projection launch");
+    if (st != QK_OK) return st;
+    st = cuda_status(lora::launch_shrink(la, x_dtype == QK_BF16, dev_id, s), "adapter shrink launch");
   } else {
+    // the GEMM's counters and split-K accumulators start at zero
+    gemm::PairPlan pl;
+    if (l.gemm > 0 && pair_plan_for(m, n, k, 0, &pl) &&
+        cudaMemsetAsync(workspace, 0, gemm::pair_workspace_zero_bytes(pl), s) != cudaSuccess)
+      return QK_ERR_CUDA;
+    st = cuda_status(lora::launch_shrink(la, x_dtype == QK_BF16, dev_id, s), "adapter shrink launch");
+    if (st != QK_OK) return st;
     st = gemm_common(m, n, k, a, b, scale_a, scale_b, 0, output_scale, const_cast<int32_t*>(la.c), nullptr,
                      out_dtype, l.gemm > 0 ? workspace : nullptr, l.gemm, stream, nullptr, nullptr);
   }

@@ -43,12 +43,12 @@ struct Plan {
 __host__ __device__ inline int stage_bytes(int nb) { return kRows * kK + nb * kK; }
 
 // Blocks a CTA takes of `tiles` tiles: an equal share, but no fewer than four
-// (64 KB) and no more than eight parts to a tile.
+// (64 KB), and no less than a quarter of a tile (its sums are read slice by slice).
 __host__ __device__ inline int share(int tiles, int num_kb, int grid) {
   const int64_t all = static_cast<int64_t>(tiles) * num_kb;
   int per = static_cast<int>((all + grid - 1) / grid);
   if (per < 4) per = 4;
-  const int least = (num_kb + 7) / 8;
+  const int least = (num_kb + 3) / 4;
   return per < least ? least : per;
 }
 
@@ -62,12 +62,13 @@ __device__ __forceinline__ int slice_of(int tile, int num_kb, int per, int bid) 
   return bid - static_cast<int>(static_cast<uint32_t>(tile) * num_kb / static_cast<uint32_t>(per));
 }
 
-// `tokens`: N side wanted of sets of n rows (experts) by k.  The grid is one
-// CTA an SM; the fewest blocks a CTA can get, those of one set, bound the slices.
-inline Plan plan(int tokens, int n, int k, int num_sms) {
+// `tokens`: N side wanted of sets of n rows (experts) by k; `ring`: bytes of the
+// ring.  The grid is one CTA an SM; the fewest blocks a CTA can get, those of one
+// set, bound the slices.
+inline Plan plan(int tokens, int n, int k, int num_sms, size_t ring = kRingBytes) {
   Plan p;
   p.nb = tokens >= kMaxTokens ? kMaxTokens : (tokens + 15) / 16 * 16;
-  const int fit = static_cast<int>(kRingBytes / stage_bytes(p.nb));
+  const int fit = static_cast<int>(ring / stage_bytes(p.nb));
   p.stages = fit < kMaxStages ? fit : kMaxStages;
   p.num_kb = (k + kK - 1) / kK;
   p.row_blocks = (n + kRows - 1) / kRows;
@@ -279,6 +280,21 @@ __device__ __forceinline__ void teardown(Bars& s) {
   __syncthreads();
   tc_fence_after();
   if ((threadIdx.x >> 5) == 1) tmem_dealloc(s.tmem_base, kTmemCols);
+}
+
+// An SM's split between L1 and shared memory does not change while a CTA runs on
+// it, so the small kernels around a stream share SMs with it only when they ask
+// for its split.  (Once per device and kernel; `slot` tells kernels of one
+// signature apart.)
+template <class K>
+inline cudaError_t shares_sm_once(K kernel, int dev, int slot) {
+  static std::atomic<unsigned long long> done[16] = {};
+  const unsigned long long bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0ull;
+  if (bit && (done[slot].load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                             cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess && bit) done[slot].fetch_or(bit, std::memory_order_acq_rel);
+  return e;
 }
 
 __device__ __forceinline__ uint8_t* ring_of(uint8_t* raw) {
