@@ -80,6 +80,7 @@ __device__ __forceinline__ int nth_bit(unsigned mask, int n) {
 // 16 rows of one adapter (or of none: -1).
 struct Group {
   int use;
+  int more;        // another follows in the CTA's list
   int tok[kTile];  // -1: no token
 };
 
@@ -120,7 +121,10 @@ __device__ __forceinline__ bool gather_unit(const Args& p, int u, bool none, Gro
       uint64_t mask = __shfl_sync(0xFFFFFFFFu, same[h], src);
       const int skip = (u - __shfl_sync(0xFFFFFFFFu, at, src)) * kTile + lane;
       const int use = __shfl_sync(0xFFFFFFFFu, id[h], src);
-      if (lane == 0) gr.use = use;
+      if (lane == 0) {
+        gr.use = use;
+        gr.more = 0;
+      }
       if (lane < kTile) {
         for (int n = 0; n < skip && mask != 0; ++n) mask &= mask - 1ull;
         gr.tok[lane] = mask != 0 ? __ffsll(static_cast<long long>(mask)) - 1 : -1;
@@ -132,8 +136,9 @@ __device__ __forceinline__ bool gather_unit(const Args& p, int u, bool none, Gro
   return found;
 }
 
-// The n-th adapter (or none) among tokens 16 t .. 16 t + 15, by warp 0.
-__device__ __forceinline__ bool tile_group(const Args& p, int t, int n, bool none, Group& gr) {
+// The n-th adapter (or none) among tokens 16 t .. 16 t + 15, by warp 0; the list
+// goes on with n + step.
+__device__ __forceinline__ bool tile_group(const Args& p, int t, int n, int step, bool none, Group& gr) {
   const int lane = threadIdx.x & 31, row = t * kTile + lane;
   const int id = (lane < kTile && row < p.m) ? adapter_of(p, row) : -2;
   const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
@@ -141,16 +146,19 @@ __device__ __forceinline__ bool tile_group(const Args& p, int t, int n, bool non
       __ballot_sync(0xFFFFFFFFu, id >= (none ? -1 : 0) && (same & ((1u << lane) - 1u)) == 0);
   if (n >= __popc(firsts)) return false;
   const int use = __shfl_sync(0xFFFFFFFFu, id, nth_bit(firsts, n));
-  if (lane == 0) gr.use = use;
+  if (lane == 0) {
+    gr.use = use;
+    gr.more = n + step < __popc(firsts) ? 1 : 0;
+  }
   if (lane < kTile) gr.tok[lane] = id == use ? row : -1;
   return true;
 }
 
-// Group n of the CTA, by all threads; false after the last.
-__device__ __forceinline__ bool next_group(const Args& p, int n, bool none, Group& gr, int& ok) {
+// Group n of the CTA, by all threads; false when there is none.
+__device__ __forceinline__ bool next_group(const Args& p, int n, int step, bool none, Group& gr, int& ok) {
   if (threadIdx.x < 32) {
     const bool found = p.beside ? (n == 0 && gather_unit(p, blockIdx.x, none, gr))
-                                : tile_group(p, blockIdx.x, n, none, gr);
+                                : tile_group(p, blockIdx.x, n, step, none, gr);
     if (threadIdx.x == 0) ok = found ? 1 : 0;
   }
   __syncthreads();
@@ -203,146 +211,163 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_kernel(Args p) 
   if (!p.beside) griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
-  if (!next_group(p, blockIdx.y, false, gr, ok)) {
-    if (p.beside) griddep_wait();
-    return;
-  }
-  const int use = gr.use, tok0 = gr.tok[g], tok1 = gr.tok[g + 8];
-  const int z = blockIdx.z % p.kparts, rg = blockIdx.z / p.kparts * kRankGroup, ranks = min(p.rank - rg, kRankGroup);
-  const int k0 = z * p.kpart, k1 = min(p.k, k0 + p.kpart);
-  const __nv_bfloat16* a = p.la + (static_cast<int64_t>(use) * p.rank + rg) * p.k;
-  float acc[RT][4];
+  for (int n = blockIdx.y; next_group(p, n, gridDim.y, false, gr, ok); n += gridDim.y) {
+    const int use = gr.use, tok0 = gr.tok[g], tok1 = gr.tok[g + 8];
+    const int z = blockIdx.z % p.kparts, rg = blockIdx.z / p.kparts * kRankGroup, ranks = min(p.rank - rg, kRankGroup);
+    const int k0 = z * p.kpart, k1 = min(p.k, k0 + p.kpart);
+    const __nv_bfloat16* a = p.la + (static_cast<int64_t>(use) * p.rank + rg) * p.k;
+    float acc[RT][4];
 #pragma unroll
-  for (int j = 0; j < RT; ++j)
+    for (int j = 0; j < RT; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-  // U steps' loads are issued together (ld_nc_v4 and mma_bf16 are volatile: they
-  // keep their order)
-  constexpr int U = RT <= 2 ? 4 : ((RT <= 4 || BF16) ? 2 : 1), ROW = NW * kShrinkStep;
-  for (int k = k0 + warp * kShrinkStep + q * 8; k < k1 + q * 8; k += U * ROW) {
-    uint4 x0[U][XV], x1[U][XV], b[U][RT];
+      for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
+    // U steps' loads are issued together (ld_nc_v4 and mma_bf16 are volatile: they
+    // keep their order)
+    constexpr int U = RT <= 2 ? 4 : ((RT <= 4 || BF16) ? 2 : 1), ROW = NW * kShrinkStep;
+    for (int k = k0 + warp * kShrinkStep + q * 8; k < k1 + q * 8; k += U * ROW) {
+      uint4 x0[U][XV], x1[U][XV], b[U][RT];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int ku = k + u * ROW;
-      const bool in = ku < k1;  // (K is a multiple of 16: the last step may be half one)
-      load_x<BF16>(p.x, static_cast<int64_t>(tok0) * p.k + ku, tok0 >= 0 && in, x0[u]);
-      load_x<BF16>(p.x, static_cast<int64_t>(tok1) * p.k + ku, tok1 >= 0 && in, x1[u]);
+      for (int u = 0; u < U; ++u) {
+        const int ku = k + u * ROW;
+        const bool in = ku < k1;  // (K is a multiple of 16: the last step may be half one)
+        load_x<BF16>(p.x, static_cast<int64_t>(tok0) * p.k + ku, tok0 >= 0 && in, x0[u]);
+        load_x<BF16>(p.x, static_cast<int64_t>(tok1) * p.k + ku, tok1 >= 0 && in, x1[u]);
 #pragma unroll
-      for (int j = 0; j < RT; ++j)
-        b[u][j] = (j * 8 < ranks && in) ? ld_nc_v4(a + static_cast<int64_t>(j * 8 + g) * p.k + ku)
-                                        : make_uint4(0, 0, 0, 0);
-    }
+        for (int j = 0; j < RT; ++j)
+          b[u][j] = (j * 8 < ranks && in) ? ld_nc_v4(a + static_cast<int64_t>(j * 8 + g) * p.k + ku)
+                                          : make_uint4(0, 0, 0, 0);
+      }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      uint32_t t0[4][TERMS], t1[4][TERMS];
-      terms_x<BF16>(x0[u], t0);
-      terms_x<BF16>(x1[u], t1);
+      for (int u = 0; u < U; ++u) {
+        uint32_t t0[4][TERMS], t1[4][TERMS];
+        terms_x<BF16>(x0[u], t0);
+        terms_x<BF16>(x1[u], t1);
 #pragma unroll
-      for (int i = 0; i < TERMS; ++i) {
-        const uint32_t f0[4] = {t0[0][i], t1[0][i], t0[1][i], t1[1][i]};
-        const uint32_t f1[4] = {t0[2][i], t1[2][i], t0[3][i], t1[3][i]};
+        for (int i = 0; i < TERMS; ++i) {
+          const uint32_t f0[4] = {t0[0][i], t1[0][i], t0[1][i], t1[1][i]};
+          const uint32_t f1[4] = {t0[2][i], t1[2][i], t0[3][i], t1[3][i]};
 #pragma unroll
-        for (int j = 0; j < RT; ++j) {
-          mma_bf16(acc[j], f0, b[u][j].x, b[u][j].y);
-          mma_bf16(acc[j], f1, b[u][j].z, b[u][j].w);
+          for (int j = 0; j < RT; ++j) {
+            mma_bf16(acc[j], f0, b[u][j].x, b[u][j].y);
+            mma_bf16(acc[j], f1, b[u][j].z, b[u][j].w);
+          }
         }
       }
     }
-  }
 #pragma unroll
-  for (int j = 0; j < RT; ++j) {
-    red[warp][g][j * 8 + 2 * q] = acc[j][0];
-    red[warp][g][j * 8 + 2 * q + 1] = acc[j][1];
-    red[warp][g + 8][j * 8 + 2 * q] = acc[j][2];
-    red[warp][g + 8][j * 8 + 2 * q + 1] = acc[j][3];
-  }
-  __syncthreads();
-  const float ls = p.lscale ? __ldg(p.lscale + use) : 1.0f;
-  float* s = p.s + static_cast<int64_t>(z) * p.m * p.rank + rg;
-  for (int i = tid; i < kTile * ranks; i += kShrinkThreads) {
-    const int row = i / ranks, r = i - row * ranks;
-    if (gr.tok[row] < 0) continue;
-    float v = 0.0f;
+    for (int j = 0; j < RT; ++j) {
+      red[warp][g][j * 8 + 2 * q] = acc[j][0];
+      red[warp][g][j * 8 + 2 * q + 1] = acc[j][1];
+      red[warp][g + 8][j * 8 + 2 * q] = acc[j][2];
+      red[warp][g + 8][j * 8 + 2 * q + 1] = acc[j][3];
+    }
+    __syncthreads();
+    const float ls = p.lscale ? __ldg(p.lscale + use) : 1.0f;
+    float* s = p.s + static_cast<int64_t>(z) * p.m * p.rank + rg;
+    for (int i = tid; i < kTile * ranks; i += kShrinkThreads) {
+      const int row = i / ranks, r = i - row * ranks;
+      if (gr.tok[row] < 0) continue;
+      float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) v += red[w][row][r];
-    s[static_cast<int64_t>(gr.tok[row]) * p.rank + r] = ls * v;
+      for (int w = 0; w < NW; ++w) v += red[w][row][r];
+      s[static_cast<int64_t>(gr.tok[row]) * p.rank + r] = ls * v;
+    }
+    if (!gr.more) break;
+    __syncthreads();  // the group and the sums are rewritten
   }
   if (p.beside) griddep_wait();
 }
 
 // ---------------------------------------------------------------------------
 // out: a CTA takes the 16 rows of a group (or one group of a tile after another)
-// by 256 columns, a warp 32 of the columns.  Column 2 q + b of the j-th product of
+// by 512 columns, a warp 32 of each half.  Column 2 q + b of the j-th product of
 // a warp stands for column 8 q + 2 j + b of its 32, so that a thread ends up with
 // 8 consecutive columns of rows g and g + 8: 16-byte reads of the sums, 16-byte
-// writes.  The adapter's rows are requested first (before the wait, which a CTA
-// that starts early spends on them: they are the caller's), then the sums' slices
-// and s.
+// writes.  The adapter's rows and the scales of both halves are requested first
+// (before the wait, which a CTA that starts early spends on them: they are the
+// caller's), then the sums and s.  (256 columns a CTA, twice as many CTAs in
+// more than one wave, took 24.5 us instead of XX for 64 tokens of 32 adapters.)
 // ---------------------------------------------------------------------------
 constexpr int kExpandThreads = 256;
-constexpr int kExpandCols = 256;
+constexpr int kHalves = 2;
+constexpr int kExpandCols = 256 * kHalves;
+constexpr int kSlices = 3;  // of the sums, at most (a CTA takes at least half of a tile)
 
 inline size_t expand_smem(int rank) { return static_cast<size_t>(3) * kTile * ((rank + 31) / 32 * 16 + 4) * 4; }
 
-__global__ void __launch_bounds__(kExpandThreads, 3) lora_expand_kernel(Args p) {
+__global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(Args p) {
   extern __shared__ uint32_t ss[];  // s: [term][row][rank / 2 words], rows padded by 16 bytes
   __shared__ Group gr;
   __shared__ int ok;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
   const int steps = (p.rank + 31) / 32, pitch = steps * 16 + 4;
-  const int col0 = blockIdx.y * kExpandCols + warp * 32, col = col0 + q * 8;
-  const bool in = col < p.n;  // (n is a multiple of 8)
-  const int slices = (in && p.per > 0) ? stream::slices_of(col / stream::kRows, p.num_kb, p.per) : 1;
+  const int col0 = blockIdx.y * kExpandCols + warp * 32;  // of the first half
   const int64_t slice = static_cast<int64_t>(p.m) * p.n;
+  float4 sw[kHalves][2];
+#pragma unroll
+  for (int v = 0; v < kHalves; ++v) {
+    const int col = col0 + v * 256 + q * 8;
+    const bool in = col < p.n;  // (n is a multiple of 8)
+    sw[v][0] = in ? __ldg(reinterpret_cast<const float4*>(p.sw + col)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    sw[v][1] = in ? __ldg(reinterpret_cast<const float4*>(p.sw + col) + 1) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
   bool waited = false;
-  for (int n = blockIdx.z; next_group(p, n, true, gr, ok); n += gridDim.z) {
+  for (int n = blockIdx.z; next_group(p, n, gridDim.z, true, gr, ok); n += gridDim.z) {
     const int use = gr.use;
     const __nv_bfloat16* b = p.lb + static_cast<int64_t>(use) * p.n * p.rank;
-    uint4 bv[4];
-    auto request = [&](int st) {  // 32 ranks of the adapter's rows
+    uint4 bv[kHalves][4];
+    auto request = [&](int v, int st) {  // 32 ranks of the adapter's rows
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int r = st * 32 + q * 8, c = col0 + (g >> 1) * 8 + j * 2 + (g & 1);
-        bv[j] = (c < p.n && r < p.rank) ? ld_nc_v4(b + static_cast<int64_t>(c) * p.rank + r) : make_uint4(0, 0, 0, 0);
+        const int r = st * 32 + q * 8, c = col0 + v * 256 + (g >> 1) * 8 + j * 2 + (g & 1);
+        bv[v][j] = (c < p.n && r < p.rank) ? ld_nc_v4(b + static_cast<int64_t>(c) * p.rank + r) : make_uint4(0, 0, 0, 0);
       }
     };
-    if (use >= 0) request(0);
+    if (use >= 0) {
+#pragma unroll
+      for (int v = 0; v < kHalves; ++v) request(v, 0);
+    }
+    float sa[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int tok = gr.tok[g + h * 8];
+      sa[h] = tok >= 0 ? __ldg(p.sa + tok) : 0.0f;
+    }
     if (!waited) {
       griddep_wait();
       griddep_launch_dependents();
       waited = true;
     }
-    int4 c0[2], c1[2];  // the sums of rows g and g + 8
+    int4 c0[kHalves][2], c1[kHalves][2];  // the sums of rows g and g + 8
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int tok = gr.tok[g + h * 8];
-      if (tok < 0 || !in) continue;
-      const int32_t* c = p.c + static_cast<int64_t>(tok) * p.n + col;
-      int4 e0[3], e1[3];
-      c0[h] = *reinterpret_cast<const int4*>(c);
-      c1[h] = *reinterpret_cast<const int4*>(c + 4);
+    for (int v = 0; v < kHalves; ++v) {
+      const int col = col0 + v * 256 + q * 8;
+      const int slices = p.per > 0 ? stream::slices_of(min(col, p.n - 1) / stream::kRows, p.num_kb, p.per) : 1;
+      int4 e0[2][kSlices - 1], e1[2][kSlices - 1];
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        const bool on = i + 1 < slices;
-        e0[i] = on ? *reinterpret_cast<const int4*>(c + (i + 1) * slice) : make_int4(0, 0, 0, 0);
-        e1[i] = on ? *reinterpret_cast<const int4*>(c + (i + 1) * slice + 4) : make_int4(0, 0, 0, 0);
+      for (int h = 0; h < 2; ++h) {
+        const int tok = gr.tok[g + h * 8];
+        const bool in = tok >= 0 && col < p.n;
+        const int4 zero = make_int4(0, 0, 0, 0);
+        const int32_t* c = p.c + static_cast<int64_t>(in ? tok : 0) * p.n + (in ? col : 0);
+        c0[v][h] = in ? *reinterpret_cast<const int4*>(c) : zero;
+        c1[v][h] = in ? *reinterpret_cast<const int4*>(c + 4) : zero;
+#pragma unroll
+        for (int i = 0; i < kSlices - 1; ++i) {
+          const bool on = in && i + 1 < slices;
+          e0[h][i] = on ? *reinterpret_cast<const int4*>(c + (i + 1) * slice) : zero;
+          e1[h][i] = on ? *reinterpret_cast<const int4*>(c + (i + 1) * slice + 4) : zero;
+        }
       }
       auto add = [](int4& x, const int4& y) { x = make_int4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w); };
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        add(c0[h], e0[i]);
-        add(c1[h], e1[i]);
-      }
-      for (int i = 4; i < slices; ++i) {
-        add(c0[h], *reinterpret_cast<const int4*>(c + i * slice));
-        add(c1[h], *reinterpret_cast<const int4*>(c + i * slice + 4));
-      }
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < kSlices - 1; ++i) {
+          add(c0[v][h], e0[h][i]);
+          add(c1[v][h], e1[h][i]);
+        }
     }
-    float d[4][4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) d[j][i] = 0.0f;
     if (use >= 0) {
       for (int i = tid; i < kTile * steps * 16; i += kExpandThreads) {
         const int row = i / (steps * 16), w = i - row * (steps * 16), r = 2 * w, tok = gr.tok[row];
@@ -365,50 +390,56 @@ __global__ void __launch_bounds__(kExpandThreads, 3) lora_expand_kernel(Args p) 
         for (int e = 0; e < 3; ++e) ss[(e * kTile + row) * pitch + w] = term[e];
       }
       __syncthreads();
-      for (int st = 0; st < steps; ++st) {
-        if (st > 0) request(st);
-        const int at = st * 16 + q * 4;
+    }
 #pragma unroll
-        for (int e = 0; e < 3; ++e) {
-          const uint4 x0 = *reinterpret_cast<const uint4*>(&ss[(e * kTile + g) * pitch + at]);
-          const uint4 x1 = *reinterpret_cast<const uint4*>(&ss[(e * kTile + g + 8) * pitch + at]);
-          const uint32_t f0[4] = {x0.x, x1.x, x0.y, x1.y}, f1[4] = {x0.z, x1.z, x0.w, x1.w};
+    for (int v = 0; v < kHalves; ++v) {
+      const int col = col0 + v * 256 + q * 8;
+      float d[4][4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            mma_bf16(d[j], f0, bv[j].x, bv[j].y);
-            mma_bf16(d[j], f1, bv[j].z, bv[j].w);
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[j][i] = 0.0f;
+      if (use >= 0) {
+        for (int st = 0; st < steps; ++st) {
+          if (st > 0) request(v, st);
+          const int at = st * 16 + q * 4;
+#pragma unroll
+          for (int e = 0; e < 3; ++e) {
+            const uint4 x0 = *reinterpret_cast<const uint4*>(&ss[(e * kTile + g) * pitch + at]);
+            const uint4 x1 = *reinterpret_cast<const uint4*>(&ss[(e * kTile + g + 8) * pitch + at]);
+            const uint32_t f0[4] = {x0.x, x1.x, x0.y, x1.y}, f1[4] = {x0.z, x1.z, x0.w, x1.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              mma_bf16(d[j], f0, bv[v][j].x, bv[v][j].y);
+              mma_bf16(d[j], f1, bv[v][j].z, bv[v][j].w);
+            }
           }
         }
       }
-    }
-    float4 sw[2] = {};
-    if (in) {
-      sw[0] = __ldg(reinterpret_cast<const float4*>(p.sw + col));
-      sw[1] = __ldg(reinterpret_cast<const float4*>(p.sw + col) + 1);
-    }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int tok = gr.tok[g + h * 8];
-      if (tok < 0 || !in) continue;
-      const int64_t o = static_cast<int64_t>(tok) * p.n + col;
-      const float sa = __ldg(p.sa + tok);
-      auto val = [&](int acc, float s, float add) {
-        const float v = __fmul_rn(__fmul_rn(__fmul_rn(__int2float_rn(acc), sa), s), p.alpha);
-        return use >= 0 ? __fadd_rn(v, add) : v;
-      };
-      const float v0 = val(c0[h].x, sw[0].x, d[0][2 * h]), v1 = val(c0[h].y, sw[0].y, d[0][2 * h + 1]);
-      const float v2 = val(c0[h].z, sw[0].z, d[1][2 * h]), v3 = val(c0[h].w, sw[0].w, d[1][2 * h + 1]);
-      const float v4 = val(c1[h].x, sw[1].x, d[2][2 * h]), v5 = val(c1[h].y, sw[1].y, d[2][2 * h + 1]);
-      const float v6 = val(c1[h].z, sw[1].z, d[3][2 * h]), v7 = val(c1[h].w, sw[1].w, d[3][2 * h + 1]);
-      if (p.out_bf16) {
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + o) =
-            make_uint4(pack_bf16x2(v0, v1), pack_bf16x2(v2, v3), pack_bf16x2(v4, v5), pack_bf16x2(v6, v7));
-      } else {
-        float4* out = reinterpret_cast<float4*>(static_cast<float*>(p.out) + o);
-        out[0] = make_float4(v0, v1, v2, v3);
-        out[1] = make_float4(v4, v5, v6, v7);
+      for (int h = 0; h < 2; ++h) {
+        const int tok = gr.tok[g + h * 8];
+        if (tok < 0 || col >= p.n) continue;
+        const int64_t o = static_cast<int64_t>(tok) * p.n + col;
+        auto val = [&](int acc, float s, float add) {
+          const float f = __fmul_rn(__fmul_rn(__fmul_rn(__int2float_rn(acc), sa[h]), s), p.alpha);
+          return use >= 0 ? __fadd_rn(f, add) : f;
+        };
+        const float v0 = val(c0[v][h].x, sw[v][0].x, d[0][2 * h]), v1 = val(c0[v][h].y, sw[v][0].y, d[0][2 * h + 1]);
+        const float v2 = val(c0[v][h].z, sw[v][0].z, d[1][2 * h]), v3 = val(c0[v][h].w, sw[v][0].w, d[1][2 * h + 1]);
+        const float v4 = val(c1[v][h].x, sw[v][1].x, d[2][2 * h]), v5 = val(c1[v][h].y, sw[v][1].y, d[2][2 * h + 1]);
+        const float v6 = val(c1[v][h].z, sw[v][1].z, d[3][2 * h]), v7 = val(c1[v][h].w, sw[v][1].w, d[3][2 * h + 1]);
+        if (p.out_bf16) {
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + o) =
+              make_uint4(pack_bf16x2(v0, v1), pack_bf16x2(v2, v3), pack_bf16x2(v4, v5), pack_bf16x2(v6, v7));
+        } else {
+          float4* out = reinterpret_cast<float4*>(static_cast<float*>(p.out) + o);
+          out[0] = make_float4(v0, v1, v2, v3);
+          out[1] = make_float4(v4, v5, v6, v7);
+        }
       }
     }
+    if (!gr.more) break;
     __syncthreads();  // the group and s are rewritten
   }
   if (!waited) griddep_wait();
@@ -453,7 +484,9 @@ inline bool streams(int m) { return m <= stream::kMaxTokens; }
 
 // (a ring of 172 KB leaves room for a CTA of s, with its 33 KB for 64 ranks)
 constexpr size_t kRing = 172 * 1024;
-inline stream::Plan stream_plan(int m, int n, int k, int num_sms) { return stream::plan(m, n, k, num_sms, kRing); }
+inline stream::Plan stream_plan(int m, int n, int k, int num_sms) {
+  return stream::plan(m, n, k, num_sms, kSlices - 1, kRing);
+}
 
 // Groups at most: of the whole batch (gathered; a token without an adapter is in
 // none or, for the output, in one more), or of a tile.
@@ -482,16 +515,21 @@ inline cudaError_t launch_shrink_rt(const Args& a, dim3 grid, int dev, cudaStrea
 }
 
 template <bool BF16>
-inline cudaError_t launch_shrink_t(const Args& a, int dev, cudaStream_t stream) {
+inline cudaError_t launch_shrink_t(const Args& a, int dev, int num_sms, cudaStream_t stream) {
   const int most = most_groups(a.m, a.adapters, false), rgroups = (a.rank + kRankGroup - 1) / kRankGroup;
-  const dim3 grid(a.beside ? most : (a.m + kTile - 1) / kTile, a.beside ? 1 : most, a.kparts * rgroups);
+  const int tiles = (a.m + kTile - 1) / kTile;
+  int y = a.beside ? 1 : 4 * num_sms / (tiles * a.kparts * rgroups);
+  y = y < 1 ? 1 : (y > most ? most : y);
+  const dim3 grid(a.beside ? most : tiles, y, a.kparts * rgroups);
   if (a.rank <= 16) return launch_shrink_rt<BF16, 2>(a, grid, dev, stream);
   if (a.rank <= 32) return launch_shrink_rt<BF16, 4>(a, grid, dev, stream);
   return launch_shrink_rt<BF16, 8>(a, grid, dev, stream);
 }
 
-inline cudaError_t launch_shrink(const Args& a, bool x_bf16, int dev, cudaStream_t stream) {
-  return x_bf16 ? launch_shrink_t<true>(a, dev, stream) : launch_shrink_t<false>(a, dev, stream);
+// A long batch's tiles take their groups one after another, unless the grid is
+// small enough for CTAs of their own (four an SM).
+inline cudaError_t launch_shrink(const Args& a, bool x_bf16, int dev, int num_sms, cudaStream_t stream) {
+  return x_bf16 ? launch_shrink_t<true>(a, dev, num_sms, stream) : launch_shrink_t<false>(a, dev, num_sms, stream);
 }
 
 // Returns 0, 1 when a tensor map could not be made, 2 with *err set.
@@ -500,6 +538,7 @@ inline int launch_stream(const Args& a, const int8_t* x, const int8_t* w, const 
   CUtensorMap tw, tx;
   if (!gemm::cached_tmap(&tw, w, a.n, a.k, stream::kRows) || !gemm::cached_tmap(&tx, x, a.m, a.k, pl.nb)) return 1;
   if ((*err = gemm::set_smem_once(lora_stream_kernel, dev, 0, stream::kRingBytes + 1024)) != cudaSuccess) return 2;
+  if ((*err = stream::shares_sm_once(lora_stream_kernel, dev, 0)) != cudaSuccess) return 2;
   *err = launch_pdl(lora_stream_kernel, dim3(num_sms), dim3(stream::kThreads), stream::smem_bytes(pl), stream, 1, tw, tx,
                     a.m, pl, const_cast<int32_t*>(a.c));
   return *err == cudaSuccess ? 0 : 2;

@@ -200,7 +200,7 @@ struct Down {
 // What kernel 4 needs of the routing (by all threads).
 __device__ __forceinline__ void write_routing(const Args& p, const Routing& r) {
   const int tid = threadIdx.x, pairs = p.m * p.topk;
-  const int per = stream::share(down_tiles(p, r), p.down.num_kb, p.down_grid);
+  const int per = stream::share(down_tiles(p, r), p.down.num_kb, p.down.cut, p.down_grid);
   for (int i = tid; i < pairs; i += blockDim.x)
     if (expert_of(p, i) < 0) p.by_pair[i] = make_int4(-1, 0, 0, 0);
   int base = 0;
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kQuantThreads) moe_quant_kernel(Args p) {
     active += __popc(used[i]);
     index += i < (e >> 5) ? __popc(used[i]) : (i == (e >> 5) ? __popc(used[i] & ((1u << (e & 31)) - 1u)) : 0);
   }
-  const int per = stream::share(active * p.up.row_blocks, p.up.num_kb, p.up_grid);
+  const int per = stream::share(active * p.up.row_blocks, p.up.num_kb, p.up.cut, p.up_grid);
   const float sa = __ldg(p.sa + ((pair * p.topk_inv) >> 16));
   int32_t* gu = p.gu + static_cast<int64_t>(pair) * 2 * p.inter;
   const int64_t slice = static_cast<int64_t>(pairs) * 2 * p.inter;
@@ -449,8 +449,9 @@ __global__ void __launch_bounds__(128) moe_combine_kernel(Args p) {
 // weights read again, from L2.
 inline void plans(Args& a, int num_sms) {
   const int64_t pairs = static_cast<int64_t>(a.m) * a.topk, share = (2 * pairs + a.experts - 1) / a.experts;
-  a.up = stream::plan(a.m, 2 * a.inter, a.hidden, num_sms);
-  a.down = stream::plan(static_cast<int>(share < a.m ? share : a.m), a.hidden, a.inter, num_sms);
+  a.up = stream::plan(a.m, 2 * a.inter, a.hidden, num_sms, 4, stream::kRingBytes);
+  a.down = stream::plan(static_cast<int>(share < a.m ? share : a.m), a.hidden, a.inter, num_sms, 4,
+                        stream::kRingBytes);
   a.up_grid = a.down_grid = num_sms;
 }
 

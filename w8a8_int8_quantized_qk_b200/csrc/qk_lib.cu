@@ -743,19 +743,19 @@ qk_status qk_w8a8_lora_gemm(int m, int n, int k, const int8_t* a, const int8_t* 
   if (la.beside) {
     const stream::Plan sp = lora::stream_plan(m, n, k, dev->sms);
     la.num_kb = sp.num_kb;
-    la.per = stream::share(sp.row_blocks, sp.num_kb, dev->sms);
+    la.per = stream::share(sp.row_blocks, sp.num_kb, sp.cut, dev->sms);
     cudaError_t e = cudaSuccess;
     const int r = lora::launch_stream(la, a, b, sp, dev_id, dev->sms, s, &e);
     st = r == 1 ? cuda_status(cudaErrorInvalidValue, "tensor map encoding") : cuda_status(e, "projection launch");
     if (st != QK_OK) return st;
-    st = cuda_status(lora::launch_shrink(la, x_dtype == QK_BF16, dev_id, s), "adapter shrink launch");
+    st = cuda_status(lora::launch_shrink(la, x_dtype == QK_BF16, dev_id, dev->sms, s), "adapter shrink launch");
   } else {
     // the GEMM's counters and split-K accumulators start at zero
     gemm::PairPlan pl;
     if (l.gemm > 0 && pair_plan_for(m, n, k, 0, &pl) &&
         cudaMemsetAsync(workspace, 0, gemm::pair_workspace_zero_bytes(pl), s) != cudaSuccess)
       return QK_ERR_CUDA;
-    st = cuda_status(lora::launch_shrink(la, x_dtype == QK_BF16, dev_id, s), "adapter shrink launch");
+    st = cuda_status(lora::launch_shrink(la, x_dtype == QK_BF16, dev_id, dev->sms, s), "adapter shrink launch");
     if (st != QK_OK) return st;
     st = gemm_common(m, n, k, a, b, scale_a, scale_b, 0, output_scale, const_cast<int32_t*>(la.c), nullptr,
                      out_dtype, l.gemm > 0 ? workspace : nullptr, l.gemm, stream, nullptr, nullptr);

@@ -37,18 +37,19 @@ struct Plan {
   int num_kb;      // K blocks of a tile
   int row_blocks;
   int n;           // weight rows (per expert)
-  int max_slices;  // parts a tile is cut into, at most
+  int cut;         // a CTA takes at least 1 / cut of a tile
+  int max_slices;  // parts a tile is then cut into, at most
 };
 
 __host__ __device__ inline int stage_bytes(int nb) { return kRows * kK + nb * kK; }
 
 // Blocks a CTA takes of `tiles` tiles: an equal share, but no fewer than four
-// (64 KB), and no less than a quarter of a tile (its sums are read slice by slice).
-__host__ __device__ inline int share(int tiles, int num_kb, int grid) {
+// (64 KB), and no less than 1 / cut of a tile (its sums are read slice by slice).
+__host__ __device__ inline int share(int tiles, int num_kb, int cut, int grid) {
   const int64_t all = static_cast<int64_t>(tiles) * num_kb;
   int per = static_cast<int>((all + grid - 1) / grid);
   if (per < 4) per = 4;
-  const int least = (num_kb + 3) / 4;
+  const int least = (num_kb + cut - 1) / cut;
   return per < least ? least : per;
 }
 
@@ -62,10 +63,10 @@ __device__ __forceinline__ int slice_of(int tile, int num_kb, int per, int bid) 
   return bid - static_cast<int>(static_cast<uint32_t>(tile) * num_kb / static_cast<uint32_t>(per));
 }
 
-// `tokens`: N side wanted of sets of n rows (experts) by k; `ring`: bytes of the
-// ring.  The grid is one CTA an SM; the fewest blocks a CTA can get, those of one
+// `tokens`: N side wanted of sets of n rows (experts) by k; `cut` as above;
+// `ring`: bytes of the ring.  The grid is one CTA an SM; the fewest blocks a CTA can get, those of one
 // set, bound the slices.
-inline Plan plan(int tokens, int n, int k, int num_sms, size_t ring = kRingBytes) {
+inline Plan plan(int tokens, int n, int k, int num_sms, int cut, size_t ring) {
   Plan p;
   p.nb = tokens >= kMaxTokens ? kMaxTokens : (tokens + 15) / 16 * 16;
   const int fit = static_cast<int>(ring / stage_bytes(p.nb));
@@ -73,7 +74,8 @@ inline Plan plan(int tokens, int n, int k, int num_sms, size_t ring = kRingBytes
   p.num_kb = (k + kK - 1) / kK;
   p.row_blocks = (n + kRows - 1) / kRows;
   p.n = n;
-  const int per = share(p.row_blocks, p.num_kb, num_sms);
+  p.cut = cut;
+  const int per = share(p.row_blocks, p.num_kb, cut, num_sms);
   // a part starts at the tile's start or at a multiple of `per` inside it
   p.max_slices = (p.num_kb - 1) / per + 2;
   return p;
@@ -136,7 +138,7 @@ __device__ __forceinline__ void run(const P& prob, const Plan& pl, Bars& s, uint
                                     const CUtensorMap* tmX) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int stages = pl.stages, sb = stage_bytes(pl.nb), num_kb = pl.num_kb;
-  const int tiles = prob.tiles(), per = share(tiles, num_kb, static_cast<int>(gridDim.x));
+  const int tiles = prob.tiles(), per = share(tiles, num_kb, pl.cut, static_cast<int>(gridDim.x));
   const uint32_t ring0 = smem_addr(ring);
   Range parts(tiles, num_kb, per);
   typename P::Walk w = prob.start();
