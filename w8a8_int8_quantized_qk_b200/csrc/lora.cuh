@@ -279,14 +279,12 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_kernel(Args p) 
 }
 
 // ---------------------------------------------------------------------------
-// out: a CTA takes the 16 rows of a group (or one group of a tile after another)
-// by 512 columns, a warp 32 of each half.  Column 2 q + b of the j-th product of
-// a warp stands for column 8 q + 2 j + b of its 32, so that a thread ends up with
-// 8 consecutive columns of rows g and g + 8: 16-byte reads of the sums, 16-byte
-// writes.  The adapter's rows and the scales of both halves are requested first
-// (before the wait, which a CTA that starts early spends on them: they are the
-// caller's), then the sums and s.  (256 columns a CTA, twice as many CTAs in
-// more than one wave, took 24.5 us instead of XX for 64 tokens of 32 adapters.)
+// out, up to 64 tokens: a CTA takes the 16 rows of a group by 512 columns, a warp
+// 32 of each half.  Column 2 q + b of the j-th product of a warp stands for column
+// 8 q + 2 j + b of its 32, so that a thread ends up with 8 consecutive columns of
+// rows g and g + 8: 16-byte reads of the sums, 16-byte writes.  The adapter's rows
+// and the scales of both halves are requested before the wait (they are the
+// caller's), then the sums and s.
 // ---------------------------------------------------------------------------
 constexpr int kExpandThreads = 256;
 constexpr int kHalves = 2;
@@ -294,6 +292,28 @@ constexpr int kExpandCols = 256 * kHalves;
 constexpr int kSlices = 3;  // of the sums, at most (a CTA takes at least half of a tile)
 
 inline size_t expand_smem(int rank) { return static_cast<size_t>(3) * kTile * ((rank + 31) / 32 * 16 + 4) * 4; }
+
+// Columns col .. col + 7 of row `row`: the sums' epilogue, in the GEMM's order, and
+// the adapter's part.
+__device__ __forceinline__ void store8(const Args& p, int row, int col, const int4& c0, const int4& c1, float sa,
+                                       const float4& w0, const float4& w1, bool adapter, float d0, float d1, float d2,
+                                       float d3, float d4, float d5, float d6, float d7) {
+  auto val = [&](int acc, float sw, float add) {
+    const float f = __fmul_rn(__fmul_rn(__fmul_rn(__int2float_rn(acc), sa), sw), p.alpha);
+    return adapter ? __fadd_rn(f, add) : f;
+  };
+  const float v0 = val(c0.x, w0.x, d0), v1 = val(c0.y, w0.y, d1), v2 = val(c0.z, w0.z, d2), v3 = val(c0.w, w0.w, d3);
+  const float v4 = val(c1.x, w1.x, d4), v5 = val(c1.y, w1.y, d5), v6 = val(c1.z, w1.z, d6), v7 = val(c1.w, w1.w, d7);
+  const int64_t o = static_cast<int64_t>(row) * p.n + col;
+  if (p.out_bf16) {
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + o) =
+        make_uint4(pack_bf16x2(v0, v1), pack_bf16x2(v2, v3), pack_bf16x2(v4, v5), pack_bf16x2(v6, v7));
+  } else {
+    float4* out = reinterpret_cast<float4*>(static_cast<float*>(p.out) + o);
+    out[0] = make_float4(v0, v1, v2, v3);
+    out[1] = make_float4(v4, v5, v6, v7);
+  }
+}
 
 __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(Args p) {
   extern __shared__ uint32_t ss[];  // s: [term][row][rank / 2 words], rows padded by 16 bytes
@@ -311,138 +331,273 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(Args p) 
     sw[v][0] = in ? __ldg(reinterpret_cast<const float4*>(p.sw + col)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     sw[v][1] = in ? __ldg(reinterpret_cast<const float4*>(p.sw + col) + 1) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   }
-  bool waited = false;
-  for (int n = blockIdx.z; next_group(p, n, gridDim.z, true, gr, ok); n += gridDim.z) {
-    const int use = gr.use;
-    const __nv_bfloat16* b = p.lb + static_cast<int64_t>(use) * p.n * p.rank;
-    uint4 bv[kHalves][4];
-    auto request = [&](int v, int st) {  // 32 ranks of the adapter's rows
+  if (!next_group(p, 0, 1, true, gr, ok)) {
+    griddep_wait();
+    return;
+  }
+  const int use = gr.use;
+  const __nv_bfloat16* b = p.lb + static_cast<int64_t>(use) * p.n * p.rank;
+  uint4 bv[kHalves][4];
+  auto request = [&](int v, int st) {  // 32 ranks of the adapter's rows
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = st * 32 + q * 8, c = col0 + v * 256 + (g >> 1) * 8 + j * 2 + (g & 1);
-        bv[v][j] = (c < p.n && r < p.rank) ? ld_nc_v4(b + static_cast<int64_t>(c) * p.rank + r) : make_uint4(0, 0, 0, 0);
-      }
-    };
-    if (use >= 0) {
-#pragma unroll
-      for (int v = 0; v < kHalves; ++v) request(v, 0);
+    for (int j = 0; j < 4; ++j) {
+      const int r = st * 32 + q * 8, c = col0 + v * 256 + (g >> 1) * 8 + j * 2 + (g & 1);
+      bv[v][j] = (c < p.n && r < p.rank) ? ld_nc_v4(b + static_cast<int64_t>(c) * p.rank + r) : make_uint4(0, 0, 0, 0);
     }
-    float sa[2];
+  };
+  if (use >= 0) {
+#pragma unroll
+    for (int v = 0; v < kHalves; ++v) request(v, 0);
+  }
+  float sa[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int tok = gr.tok[g + h * 8];
+    sa[h] = tok >= 0 ? __ldg(p.sa + tok) : 0.0f;
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  int4 c0[kHalves][2], c1[kHalves][2];  // the sums of rows g and g + 8
+#pragma unroll
+  for (int v = 0; v < kHalves; ++v) {
+    const int col = col0 + v * 256 + q * 8;
+    const int slices = p.per > 0 ? stream::slices_of(min(col, p.n - 1) / stream::kRows, p.num_kb, p.per) : 1;
+    int4 e0[2][kSlices - 1], e1[2][kSlices - 1];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int tok = gr.tok[g + h * 8];
-      sa[h] = tok >= 0 ? __ldg(p.sa + tok) : 0.0f;
-    }
-    if (!waited) {
-      griddep_wait();
-      griddep_launch_dependents();
-      waited = true;
-    }
-    int4 c0[kHalves][2], c1[kHalves][2];  // the sums of rows g and g + 8
+      const bool in = tok >= 0 && col < p.n;
+      const int4 zero = make_int4(0, 0, 0, 0);
+      const int32_t* c = p.c + static_cast<int64_t>(in ? tok : 0) * p.n + (in ? col : 0);
+      c0[v][h] = in ? *reinterpret_cast<const int4*>(c) : zero;
+      c1[v][h] = in ? *reinterpret_cast<const int4*>(c + 4) : zero;
 #pragma unroll
-    for (int v = 0; v < kHalves; ++v) {
-      const int col = col0 + v * 256 + q * 8;
-      const int slices = p.per > 0 ? stream::slices_of(min(col, p.n - 1) / stream::kRows, p.num_kb, p.per) : 1;
-      int4 e0[2][kSlices - 1], e1[2][kSlices - 1];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int tok = gr.tok[g + h * 8];
-        const bool in = tok >= 0 && col < p.n;
-        const int4 zero = make_int4(0, 0, 0, 0);
-        const int32_t* c = p.c + static_cast<int64_t>(in ? tok : 0) * p.n + (in ? col : 0);
-        c0[v][h] = in ? *reinterpret_cast<const int4*>(c) : zero;
-        c1[v][h] = in ? *reinterpret_cast<const int4*>(c + 4) : zero;
-#pragma unroll
-        for (int i = 0; i < kSlices - 1; ++i) {
-          const bool on = in && i + 1 < slices;
-          e0[h][i] = on ? *reinterpret_cast<const int4*>(c + (i + 1) * slice) : zero;
-          e1[h][i] = on ? *reinterpret_cast<const int4*>(c + (i + 1) * slice + 4) : zero;
-        }
+      for (int i = 0; i < kSlices - 1; ++i) {
+        const bool on = in && i + 1 < slices;
+        e0[h][i] = on ? *reinterpret_cast<const int4*>(c + (i + 1) * slice) : zero;
+        e1[h][i] = on ? *reinterpret_cast<const int4*>(c + (i + 1) * slice + 4) : zero;
       }
-      auto add = [](int4& x, const int4& y) { x = make_int4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w); };
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < kSlices - 1; ++i) {
-          add(c0[v][h], e0[h][i]);
-          add(c1[v][h], e1[h][i]);
-        }
     }
+    auto add = [](int4& x, const int4& y) { x = make_int4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w); };
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < kSlices - 1; ++i) {
+        add(c0[v][h], e0[h][i]);
+        add(c1[v][h], e1[h][i]);
+      }
+  }
+  if (use >= 0) {
+    for (int i = tid; i < kTile * steps * 16; i += kExpandThreads) {
+      const int row = i / (steps * 16), w = i - row * (steps * 16), r = 2 * w, tok = gr.tok[row];
+      uint32_t term[3] = {0, 0, 0};
+      if (tok >= 0 && r < p.rank) {
+        const float* s = p.s + static_cast<int64_t>(tok) * p.rank + r;
+        float2 f[kMaxParts];
+#pragma unroll
+        for (int z = 0; z < kMaxParts; ++z)
+          f[z] = z < p.kparts ? *reinterpret_cast<const float2*>(s + static_cast<int64_t>(z) * p.m * p.rank)
+                              : make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int z = 1; z < kMaxParts; ++z) {
+          f[0].x += f[z].x;
+          f[0].y += f[z].y;
+        }
+        split3(f[0].x, f[0].y, term);
+      }
+#pragma unroll
+      for (int e = 0; e < 3; ++e) ss[(e * kTile + row) * pitch + w] = term[e];
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int v = 0; v < kHalves; ++v) {
+    const int col = col0 + v * 256 + q * 8;
+    float d[4][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[j][i] = 0.0f;
     if (use >= 0) {
-      for (int i = tid; i < kTile * steps * 16; i += kExpandThreads) {
-        const int row = i / (steps * 16), w = i - row * (steps * 16), r = 2 * w, tok = gr.tok[row];
-        uint32_t term[3] = {0, 0, 0};
-        if (tok >= 0 && r < p.rank) {
-          const float* s = p.s + static_cast<int64_t>(tok) * p.rank + r;
-          float2 f[kMaxParts];
+      for (int st = 0; st < steps; ++st) {
+        if (st > 0) request(v, st);
+        const int at = st * 16 + q * 4;
 #pragma unroll
-          for (int z = 0; z < kMaxParts; ++z)
-            f[z] = z < p.kparts ? *reinterpret_cast<const float2*>(s + static_cast<int64_t>(z) * p.m * p.rank)
-                                : make_float2(0.0f, 0.0f);
+        for (int e = 0; e < 3; ++e) {
+          const uint4 x0 = *reinterpret_cast<const uint4*>(&ss[(e * kTile + g) * pitch + at]);
+          const uint4 x1 = *reinterpret_cast<const uint4*>(&ss[(e * kTile + g + 8) * pitch + at]);
+          const uint32_t f0[4] = {x0.x, x1.x, x0.y, x1.y}, f1[4] = {x0.z, x1.z, x0.w, x1.w};
 #pragma unroll
-          for (int z = 1; z < kMaxParts; ++z) {
-            f[0].x += f[z].x;
-            f[0].y += f[z].y;
+          for (int j = 0; j < 4; ++j) {
+            mma_bf16(d[j], f0, bv[v][j].x, bv[v][j].y);
+            mma_bf16(d[j], f1, bv[v][j].z, bv[v][j].w);
           }
-          split3(f[0].x, f[0].y, term);
         }
-#pragma unroll
-        for (int e = 0; e < 3; ++e) ss[(e * kTile + row) * pitch + w] = term[e];
       }
-      __syncthreads();
     }
 #pragma unroll
-    for (int v = 0; v < kHalves; ++v) {
-      const int col = col0 + v * 256 + q * 8;
+    for (int h = 0; h < 2; ++h) {
+      const int tok = gr.tok[g + h * 8];
+      if (tok < 0 || col >= p.n) continue;
+      store8(p, tok, col, c0[v][h], c1[v][h], sa[h], sw[v][0], sw[v][1], use >= 0, d[0][2 * h], d[0][2 * h + 1],
+             d[1][2 * h], d[1][2 * h + 1], d[2][2 * h], d[2][2 * h + 1], d[3][2 * h], d[3][2 * h + 1]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// out, longer batches: a CTA walks tiles of 16 tokens in a row at its 256 columns,
+// with the next tile's ids, sums and s in flight while the current one is
+// multiplied and stored, so that it reads and writes without a pause; an
+// adapter's rows stay in registers from tile to tile (up to 32 ranks).  Each
+// adapter of a tile is multiplied with all 16 rows, and the rows that use it take
+// its result: by selection, not by multiplying with zero, so that an adapter that
+// holds NaN or infinity reaches no row of another.  (A CTA per tile, each with its
+// own chain of loads, took 43 us for 4096 x 4096 where this takes XX.)
+// ---------------------------------------------------------------------------
+template <int RK>  // ranks, rounded up to 16, 32, 64 or 128
+__global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Args p) {
+  // ranks a thread takes of a step (as two instructions' operands, or one's)
+  constexpr int STEP = RK < 32 ? 16 : 32, STEPS = RK / STEP, HALVES = STEP / 16, VEC = STEP / 4;
+  constexpr int WORDS = RK / 2, PITCH = WORDS + 4, SV = (kTile * WORDS + kExpandThreads - 1) / kExpandThreads;
+  __shared__ __align__(16) uint32_t ss[2][3][kTile][PITCH];  // s: [buffer][term][row][pair of ranks]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  const int tiles = (p.m + kTile - 1) / kTile, col0 = blockIdx.y * 256 + warp * 32, col = col0 + q * 8;
+  const bool in = col < p.n;  // (n is a multiple of 8)
+  float4 sw[2] = {};
+  if (in) {
+    sw[0] = __ldg(reinterpret_cast<const float4*>(p.sw + col));
+    sw[1] = __ldg(reinterpret_cast<const float4*>(p.sw + col) + 1);
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  // what a tile needs, requested a tile ahead
+  int id_n = -1;
+  float sa_n[2];
+  int4 c_n[2][2];
+  float2 s_n[SV];
+  auto fetch = [&](int t) {
+    const int r0 = t * kTile;
+    id_n = (lane < kTile && t < tiles) ? adapter_of(p, r0 + lane) : -1;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = r0 + g + h * 8;
+      const bool on = t < tiles && row < p.m;
+      const int32_t* c = p.c + static_cast<int64_t>(row) * p.n + col;
+      sa_n[h] = on ? __ldg(p.sa + row) : 0.0f;
+      c_n[h][0] = on && in ? *reinterpret_cast<const int4*>(c) : make_int4(0, 0, 0, 0);
+      c_n[h][1] = on && in ? *reinterpret_cast<const int4*>(c + 4) : make_int4(0, 0, 0, 0);
+    }
+    // (s of tokens without an adapter holds anything: their rows take no product)
+#pragma unroll
+    for (int i = 0; i < SV; ++i) {
+      const int at = tid + i * kExpandThreads, row = at / WORDS, r = 2 * (at % WORDS);
+      s_n[i] = make_float2(0.0f, 0.0f);
+      if (row < kTile && r < p.rank && t < tiles && r0 + row < p.m) {
+        const float* s = p.s + static_cast<int64_t>(r0 + row) * p.rank + r;
+        s_n[i] = *reinterpret_cast<const float2*>(s);
+        for (int z = 1; z < p.kparts; ++z) {
+          const float2 f = *reinterpret_cast<const float2*>(s + static_cast<int64_t>(z) * p.m * p.rank);
+          s_n[i].x += f.x;
+          s_n[i].y += f.y;
+        }
+      }
+    }
+  };
+  fetch(blockIdx.x);
+  uint32_t bv[4][VEC / 2];
+  int held = -1;  // the adapter whose first ranks are in bv
+  int par = 0;
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x, par ^= 1) {
+    const int id = id_n, r0 = t * kTile;
+    const float sa[2] = {sa_n[0], sa_n[1]};
+    const int4 c[2][2] = {{c_n[0][0], c_n[0][1]}, {c_n[1][0], c_n[1][1]}};
+    const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
+    unsigned firsts = __ballot_sync(0xFFFFFFFFu, id >= 0 && (same & ((1u << lane) - 1u)) == 0);
+#pragma unroll
+    for (int i = 0; i < SV; ++i) {
+      const int at = tid + i * kExpandThreads;
+      if (at < kTile * WORDS) {
+        uint32_t term[3];
+        split3(s_n[i].x, s_n[i].y, term);
+#pragma unroll
+        for (int e = 0; e < 3; ++e) ss[par][e][at / WORDS][at % WORDS] = term[e];
+      }
+    }
+    fetch(t + gridDim.x);
+    __syncthreads();
+    const int id0 = __shfl_sync(0xFFFFFFFFu, id, g), id1 = __shfl_sync(0xFFFFFFFFu, id, g + 8);
+    float add[4][4];
+    bool first = true;
+    while (firsts != 0) {
+      const int use = __shfl_sync(0xFFFFFFFFu, id, __ffs(firsts) - 1);
+      firsts &= firsts - 1u;
+      const __nv_bfloat16* b = p.lb + static_cast<int64_t>(use) * p.n * p.rank;
       float d[4][4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[j][i] = 0.0f;
-      if (use >= 0) {
-        for (int st = 0; st < steps; ++st) {
-          if (st > 0) request(v, st);
-          const int at = st * 16 + q * 4;
 #pragma unroll
-          for (int e = 0; e < 3; ++e) {
-            const uint4 x0 = *reinterpret_cast<const uint4*>(&ss[(e * kTile + g) * pitch + at]);
-            const uint4 x1 = *reinterpret_cast<const uint4*>(&ss[(e * kTile + g + 8) * pitch + at]);
-            const uint32_t f0[4] = {x0.x, x1.x, x0.y, x1.y}, f1[4] = {x0.z, x1.z, x0.w, x1.w};
+      for (int st = 0; st < STEPS; ++st) {
+        if (STEPS > 1 || held != use) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              mma_bf16(d[j], f0, bv[v][j].x, bv[v][j].y);
-              mma_bf16(d[j], f1, bv[v][j].z, bv[v][j].w);
+          for (int j = 0; j < 4; ++j) {
+            const int r = st * STEP + q * VEC, cb = col0 + (g >> 1) * 8 + j * 2 + (g & 1);
+            const bool on = cb < p.n && r < p.rank;
+            const __nv_bfloat16* at = b + static_cast<int64_t>(cb) * p.rank + r;
+            if constexpr (HALVES == 2) {
+              const uint4 v = on ? __ldg(reinterpret_cast<const uint4*>(at)) : make_uint4(0, 0, 0, 0);
+              bv[j][0] = v.x;
+              bv[j][1] = v.y;
+              bv[j][2] = v.z;
+              bv[j][3] = v.w;
+            } else {
+              const uint2 v = on ? __ldg(reinterpret_cast<const uint2*>(at)) : make_uint2(0, 0);
+              bv[j][0] = v.x;
+              bv[j][1] = v.y;
             }
           }
         }
-      }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int tok = gr.tok[g + h * 8];
-        if (tok < 0 || col >= p.n) continue;
-        const int64_t o = static_cast<int64_t>(tok) * p.n + col;
-        auto val = [&](int acc, float s, float add) {
-          const float f = __fmul_rn(__fmul_rn(__fmul_rn(__int2float_rn(acc), sa[h]), s), p.alpha);
-          return use >= 0 ? __fadd_rn(f, add) : f;
-        };
-        const float v0 = val(c0[v][h].x, sw[v][0].x, d[0][2 * h]), v1 = val(c0[v][h].y, sw[v][0].y, d[0][2 * h + 1]);
-        const float v2 = val(c0[v][h].z, sw[v][0].z, d[1][2 * h]), v3 = val(c0[v][h].w, sw[v][0].w, d[1][2 * h + 1]);
-        const float v4 = val(c1[v][h].x, sw[v][1].x, d[2][2 * h]), v5 = val(c1[v][h].y, sw[v][1].y, d[2][2 * h + 1]);
-        const float v6 = val(c1[v][h].z, sw[v][1].z, d[3][2 * h]), v7 = val(c1[v][h].w, sw[v][1].w, d[3][2 * h + 1]);
-        if (p.out_bf16) {
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + o) =
-              make_uint4(pack_bf16x2(v0, v1), pack_bf16x2(v2, v3), pack_bf16x2(v4, v5), pack_bf16x2(v6, v7));
-        } else {
-          float4* out = reinterpret_cast<float4*>(static_cast<float*>(p.out) + o);
-          out[0] = make_float4(v0, v1, v2, v3);
-          out[1] = make_float4(v4, v5, v6, v7);
+        for (int e = 0; e < 3; ++e) {
+          uint32_t x0[VEC / 2], x1[VEC / 2];
+          const uint32_t* a0 = &ss[par][e][g][st * (STEP / 2) + q * (VEC / 2)];
+          const uint32_t* a1 = &ss[par][e][g + 8][st * (STEP / 2) + q * (VEC / 2)];
+          if constexpr (HALVES == 2) {
+            *reinterpret_cast<uint4*>(x0) = *reinterpret_cast<const uint4*>(a0);
+            *reinterpret_cast<uint4*>(x1) = *reinterpret_cast<const uint4*>(a1);
+          } else {
+            *reinterpret_cast<uint2*>(x0) = *reinterpret_cast<const uint2*>(a0);
+            *reinterpret_cast<uint2*>(x1) = *reinterpret_cast<const uint2*>(a1);
+          }
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h) {
+            const uint32_t f[4] = {x0[2 * h], x1[2 * h], x0[2 * h + 1], x1[2 * h + 1]};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mma_bf16(d[j], f, bv[j][2 * h], bv[j][2 * h + 1]);
+          }
         }
       }
+      held = use;
+      // (the first adapter's result goes to every row: rows of another are overwritten
+      // by theirs, rows without one do not take it)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (first || (i < 2 ? id0 : id1) == use) add[j][i] = d[j][i];
+      first = false;
     }
-    if (!gr.more) break;
-    __syncthreads();  // the group and s are rewritten
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = r0 + g + h * 8;
+      if (row < p.m && in)
+        store8(p, row, col, c[h][0], c[h][1], sa[h], sw[0], sw[1], (h ? id1 : id0) >= 0,
+               add[0][2 * h], add[0][2 * h + 1], add[1][2 * h], add[1][2 * h + 1], add[2][2 * h], add[2][2 * h + 1],
+               add[3][2 * h], add[3][2 * h + 1]);
+    }
   }
-  if (!waited) griddep_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -544,15 +699,20 @@ inline int launch_stream(const Args& a, const int8_t* x, const int8_t* w, const 
   return *err == cudaSuccess ? 0 : 2;
 }
 
-// A long batch's tiles take their groups one after another, unless the grid is
-// small enough for CTAs of their own (sixteen an SM).
 inline cudaError_t launch_expand(const Args& a, int num_sms, cudaStream_t stream) {
-  const int most = most_groups(a.m, a.adapters, true);
-  const int64_t tiles = a.beside ? most : (a.m + kTile - 1) / kTile, cols = (a.n + kExpandCols - 1) / kExpandCols;
-  int64_t z = a.beside ? 1 : 16LL * num_sms / (tiles * cols);
-  z = z < 1 ? 1 : (z > most ? most : z);
-  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(cols), static_cast<unsigned>(z));
-  return launch_pdl(lora_expand_kernel, grid, dim3(kExpandThreads), expand_smem(a.rank), stream, 1, a);
+  if (a.beside) {
+    const dim3 grid(most_groups(a.m, a.adapters, true), (a.n + kExpandCols - 1) / kExpandCols);
+    return launch_pdl(lora_expand_kernel, grid, dim3(kExpandThreads), expand_smem(a.rank), stream, 1, a);
+  }
+  // as many CTAs as are resident at once (two an SM), at least one a column block
+  const int tiles = (a.m + kTile - 1) / kTile, cols = (a.n + 255) / 256;
+  int x = 2 * num_sms / cols;
+  x = x < 1 ? 1 : (x > tiles ? tiles : x);
+  const dim3 grid(x, cols), block(kExpandThreads);
+  if (a.rank <= 16) return launch_pdl(lora_expand_long_kernel<16>, grid, block, 0, stream, 1, a);
+  if (a.rank <= 32) return launch_pdl(lora_expand_long_kernel<32>, grid, block, 0, stream, 1, a);
+  if (a.rank <= 64) return launch_pdl(lora_expand_long_kernel<64>, grid, block, 0, stream, 1, a);
+  return launch_pdl(lora_expand_long_kernel<128>, grid, block, 0, stream, 1, a);
 }
 
 }  // namespace lora

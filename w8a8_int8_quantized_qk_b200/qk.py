@@ -595,13 +595,13 @@ def _rows(t, dev, dtype, shape, what) -> int:
 
 
 def _on(dev: int, stream):
-    """None where `dev` is current and no other stream is asked for, else a context that makes it so."""
+    """The context that makes `stream` (a torch stream, or None), or `dev`'s own, current."""
     torch = _torch()
-    if stream is not None:
-        if stream.device.index != dev:
-            raise ValueError(f"stream of device {stream.device.index}, tensors on {dev}")
-        return torch.cuda.stream(stream)
-    return torch.cuda.device(dev) if torch.cuda.current_device() != dev else None
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"stream of device {stream.device.index}, tensors on {dev}")
+    return torch.cuda.stream(stream)
 
 
 def _raw_stream(dev: int) -> int:
@@ -609,46 +609,60 @@ def _raw_stream(dev: int) -> int:
 
 
 def _rmsnorm_quant(x, weight, residual, eps, scale_ub, want_norm, residual_out, norm_out, q, scale, stream, fp8):
+    torch = _torch()
     dev = x.get_device()
     if dev < 0:
         _need_cuda(x)
-    on = _on(dev, stream)
-    if on is not None:
-        with on:
+    if stream is not None or torch.cuda.current_device() != dev:
+        with _on(dev, stream):
             return _rmsnorm_quant(x, weight, residual, eps, scale_ub, want_norm, residual_out, norm_out, q, scale,
                                   None, fp8)
-    torch = _torch()
     shape, dt = x.shape, x.dtype
-    code = _dtype_code(x)
     if len(shape) != 2:
         raise ValueError(f"x: expected [m, k], got {tuple(shape)}")
     m, k = shape
-    ld_x = _rows(x, dev, dt, shape, "x")
+    code = _dtype_code(x)
+    codes = torch.uint8 if fp8 else torch.int8
     ld_res = ld_out = 0
+    res_ptr = out_ptr = norm_ptr = None
     if residual is not None:
         ld_res = _rows(residual, dev, dt, shape, "residual")
+        res_ptr = residual.data_ptr()
         if residual_out is None:
-            residual_out, ld_out = torch.empty(shape, dtype=dt, device=x.device), k
+            # (empty_like is the cheapest allocation; of rows in a wider buffer it is dense)
+            residual_out, ld_out = torch.empty_like(residual), k
+            if not residual_out.is_contiguous():
+                residual_out = torch.empty(shape, dtype=dt, device=x.device)
         else:
             ld_out = _rows(residual_out, dev, dt, shape, "residual_out")
+        out_ptr = residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out: needs a residual")
     if norm_out is not None:
-        _dense(norm_out, dev, dt, shape, "norm_out")
+        norm_ptr = _dense(norm_out, dev, dt, shape, "norm_out")
     elif want_norm:
-        norm_out = torch.empty(shape, dtype=dt, device=x.device)
-    codes = torch.uint8 if fp8 else torch.int8
-    q = torch.empty(shape, dtype=codes, device=x.device) if q is None else q
-    scale = torch.empty((m,), dtype=torch.float32, device=x.device) if scale is None else scale
-    args = [m, k, x.data_ptr(), ld_x, None if residual is None else residual.data_ptr(), ld_res, code,
-            _dense(weight, dev, dt, (k,), "weight"), eps,
-            None if residual_out is None else residual_out.data_ptr(), ld_out,
-            None if norm_out is None else norm_out.data_ptr()]
-    if fp8:
-        args.append(None if scale_ub is None else _dense(scale_ub, dev, torch.float32, (1,), "scale_ub"))
-    args += (_dense(q, dev, codes, shape, "q"), _dense(scale, dev, torch.float32, (m,), "scale"), _raw_stream(dev))
+        norm_out = torch.empty(m, k, dtype=dt, device=x.device)
+        norm_ptr = norm_out.data_ptr()
+    if q is None:
+        q = torch.empty(m, k, dtype=codes, device=x.device)
+    else:
+        _dense(q, dev, codes, shape, "q")
+    if scale is None:
+        scale = torch.empty(m, dtype=torch.float32, device=x.device)
+    else:
+        _dense(scale, dev, torch.float32, (m,), "scale")
     L = lib()
-    st = (L.qk_add_rmsnorm_quant_per_token_fp8 if fp8 else L.qk_add_rmsnorm_quant_per_token)(*args)
+    if fp8:
+        ub = None if scale_ub is None else _dense(scale_ub, dev, torch.float32, (1,), "scale_ub")
+        st = L.qk_add_rmsnorm_quant_per_token_fp8(
+            m, k, x.data_ptr(), _rows(x, dev, dt, shape, "x"), res_ptr, ld_res, code,
+            _dense(weight, dev, dt, (k,), "weight"), eps, out_ptr, ld_out, norm_ptr, ub, q.data_ptr(),
+            scale.data_ptr(), _raw_stream(dev))
+    else:
+        st = L.qk_add_rmsnorm_quant_per_token(
+            m, k, x.data_ptr(), _rows(x, dev, dt, shape, "x"), res_ptr, ld_res, code,
+            _dense(weight, dev, dt, (k,), "weight"), eps, out_ptr, ld_out, norm_ptr, q.data_ptr(),
+            scale.data_ptr(), _raw_stream(dev))
     if st != QK_OK:
         raise QKError(st, "qk_add_rmsnorm_quant_per_token" + ("_fp8" if fp8 else ""))
     return q, scale, residual_out, norm_out
@@ -677,7 +691,8 @@ def _workspace(workspace, need: int, dev: int, device):
     if workspace is None:
         if not need:
             return None, 0, None
-        workspace = _torch().empty((need,), dtype=_torch().uint8, device=device)
+        torch = _torch()
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
         return workspace.data_ptr(), need, workspace
     if workspace.get_device() != dev:
         _refuse(workspace, dev, workspace.dtype, workspace.shape, "workspace")
@@ -692,12 +707,11 @@ def w8a8_lora_gemm(a, b, scale_a, scale_b, x, lora_a, lora_b, adapter_ids, lora_
     dev = a.get_device()
     if dev < 0:
         _need_cuda(a)
-    on = _on(dev, stream)
-    if on is not None:
-        with on:
+    torch = _torch()
+    if stream is not None or torch.cuda.current_device() != dev:
+        with _on(dev, stream):
             return w8a8_lora_gemm(a, b, scale_a, scale_b, x, lora_a, lora_b, adapter_ids, lora_scale, output_scale,
                                   out_dtype, out, workspace)
-    torch = _torch()
     if a.dim() != 2 or b.dim() != 2 or lora_a.dim() != 3:
         raise ValueError("expected a [m, k], b [n, k] and lora_a [adapters, rank, k]")
     m, k = a.shape
@@ -706,7 +720,7 @@ def w8a8_lora_gemm(a, b, scale_a, scale_b, x, lora_a, lora_b, adapter_ids, lora_
     i8, f32, bf16 = torch.int8, torch.float32, torch.bfloat16
     x_code = _dtype_code(x)
     if out is None:
-        out = torch.empty((m, n), dtype=bf16 if out_dtype is None else out_dtype, device=a.device)
+        out = torch.empty(m, n, dtype=bf16 if out_dtype is None else out_dtype, device=a.device)
     L = lib()
     ws, ws_bytes, hold = _workspace(workspace, L.qk_w8a8_lora_gemm_workspace_size(m, n, k, rank), dev, a.device)
     st = L.qk_w8a8_lora_gemm(
@@ -732,12 +746,11 @@ def w8a8_moe_layer(a, scale_a, topk_ids, topk_weights, w_gate_up, scale_gate_up,
     dev = a.get_device()
     if dev < 0:
         _need_cuda(a)
-    on = _on(dev, stream)
-    if on is not None:
-        with on:
+    torch = _torch()
+    if stream is not None or torch.cuda.current_device() != dev:
+        with _on(dev, stream):
             return w8a8_moe_layer(a, scale_a, topk_ids, topk_weights, w_gate_up, scale_gate_up, w_down, scale_down,
                                   out_dtype, out, workspace)
-    torch = _torch()
     if a.dim() != 2 or topk_ids.dim() != 2 or w_down.dim() != 3:
         raise ValueError("expected a [m, hidden], topk_ids [m, topk] and w_down [experts, hidden, inter]")
     m, hidden = a.shape
@@ -745,7 +758,7 @@ def w8a8_moe_layer(a, scale_a, topk_ids, topk_weights, w_gate_up, scale_gate_up,
     experts, _, inter = w_down.shape
     i8, f32 = torch.int8, torch.float32
     if out is None:
-        out = torch.empty((m, hidden), dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=a.device)
+        out = torch.empty(m, hidden, dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=a.device)
     L = lib()
     ws, ws_bytes, hold = _workspace(workspace, L.qk_w8a8_moe_layer_workspace_size(m, hidden, inter, experts, topk),
                                     dev, a.device)
