@@ -199,7 +199,8 @@ QK_API qk_status qk_silu_mul_quant_per_token_fp8(int m, int k, const void* gate,
  * residual_out   optional [m, k] x_dtype, row stride ld_res_out (>= k): r;
  *                needs a residual; may be residual or x itself (same pointer
  *                and stride), and may overlap nothing else
- * norm_out       optional [m, k] x_dtype, dense
+ * norm_out       optional [m, k] x_dtype, dense; like q and scale it may overlap
+ *                no input
  * q, scale       [m, k] int8 (e4m3 codes), dense, and [m] fp32
  * scale_ub       fp8: optional device pointer to one fp32 bound (> 0)
  * 16-byte aligned: x, residual, weight, residual_out, norm_out, q, and every
@@ -395,7 +396,7 @@ QK_API qk_status qk_w8a8_moe_gemm(int num_experts, int total_m, int n, int k, in
  * adapter.
  *
  * m, n, k, a, b, scale_a, scale_b, output_scale, out   as qk_w8a8_gemm with
- *                group_k = 0 (out required)
+ *                group_k = 0 (out required; n above 16776960: QK_ERR_UNSUPPORTED)
  * x              [m, k] x_dtype, dense, 16-B aligned: the tokens before their
  *                quantisation (norm_out of the fused norm, say)
  * num_adapters   >= 1

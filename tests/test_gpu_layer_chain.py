@@ -137,6 +137,59 @@ def test_on_another_stream(m):
         assert same(again, full)
 
 
+def test_one_workspace_for_calls_of_all_kinds():
+    """A workspace used again by the next call on the stream, while the last one's kernels still run: tokens
+    without any expert or adapter (kernels with nothing to do end at once) between ordinary ones."""
+    need_gpu()
+    w = weights(8)
+    kinds = []
+    for k, m in enumerate((6, 64, 1, 17)):
+        t = tokens(m, 60 + k)
+        a, sa = qk.quantize_per_token(t["x"])
+        for none in (False, True):
+            top = torch.full_like(t["top"], -1) if none else t["top"]
+            ids = torch.full_like(t["ids"], -1) if none else t["ids"]
+            kinds.append((lambda ws, a=a, sa=sa, top=top, t=t: qk.w8a8_moe_layer(
+                a, sa, top, t["wt"], w["w13"], w["s13"], w["w2"], w["s2"], workspace=ws),
+                lambda ws, a=a, sa=sa, ids=ids, t=t: qk.w8a8_lora_gemm(
+                    a, w["w"], sa, w["sw"], t["x"], w["la"], w["lb"], ids, workspace=ws)))
+    big = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    want = []
+    for pair in kinds:
+        for call in pair:
+            want.append(call(None))
+            torch.cuda.synchronize()
+    for _ in range(10):
+        big.fill_(255)
+        got = [call(big) for pair in kinds for call in pair]
+        assert same(got, want)
+
+
+def test_projection_captured_with_split_k():
+    """The GEMM's own workspace has to be cleared in the replay too."""
+    need_gpu()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    m, n, k = 300, 2304, 512
+    x = torch.randn((m, k), generator=g, device="cuda").bfloat16()
+    b = torch.randint(-127, 128, (n, k), generator=g, device="cuda", dtype=torch.int8)
+    sw = torch.rand(n, generator=g, device="cuda") / 1000
+    la = (torch.randn((2, 8, k), generator=g, device="cuda") / 20).bfloat16()
+    lb = torch.randn((2, n, 8), generator=g, device="cuda").bfloat16()
+    ids = torch.randint(-1, 2, (m,), generator=g, device="cuda", dtype=torch.int32)
+    a, sa = qk.quantize_per_token(x)
+    want = qk.w8a8_lora_gemm(a, b, sa, sw, x, la, lb, ids)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = qk.w8a8_lora_gemm(a, b, sa, sw, x, la, lb, ids)
+    for _ in range(5):
+        out.zero_()
+        graph.replay()
+        graph.replay()
+        assert torch.equal(out, want)
+    del graph
+
+
 def test_from_several_threads():
     """Calls of several threads on one stream and on their own: each has its own workspace."""
     need_gpu()

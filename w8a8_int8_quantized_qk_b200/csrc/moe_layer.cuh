@@ -279,7 +279,10 @@ __global__ void __launch_bounds__(kQuantThreads) moe_quant_kernel(Args p) {
     pair = blockIdx.x / ranks;
   }
   const int tid = threadIdx.x, pairs = p.m * p.topk, e = expert_of(p, pair);
-  if (e < 0) return;  // (the whole cluster)
+  if (e < 0) {  // (the whole cluster) still, this kernel ends only after kernel 1
+    griddep_wait();
+    return;
+  }
   // (ids and scales are the caller's: complete before kernel 1 let this one start)
   if (tid < kMaxExperts / 32) used[tid] = 0;
   if (tid == 0) place = 0;

@@ -679,10 +679,14 @@ LoraLayout lora_layout(int m, int n, int k, int rank, int num_sms) {
   return l;
 }
 
+// (blocks of 256 columns are a grid's second dimension)
+constexpr int kLoraMaxN = 65535 * 256;
+
 qk_status lora_check(int m, int n, int k, int rank) {
   const qk_status st = gemm_check(m, n, k, 0);
   if (st != QK_OK) return st;
-  return (rank < 8 || rank > 128 || (rank % 8) != 0) ? QK_ERR_INVALID_ARG : QK_OK;
+  if (rank < 8 || rank > 128 || (rank % 8) != 0) return QK_ERR_INVALID_ARG;
+  return n > kLoraMaxN ? QK_ERR_UNSUPPORTED : QK_OK;
 }
 }  // namespace
 

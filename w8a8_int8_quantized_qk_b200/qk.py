@@ -18,6 +18,7 @@ fallback: a missing library or a non-CUDA tensor raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -686,6 +687,12 @@ def add_rmsnorm_quant_per_token_fp8(x, weight, residual=None, eps: float = 1e-6,
                           True)
 
 
+@functools.lru_cache(maxsize=1024)
+def _size(query: str, dev: int, *sizes) -> int:
+    """A workspace size query's answer (it depends on the sizes and the device alone, which is current)."""
+    return getattr(lib(), query)(*sizes)
+
+
 def _workspace(workspace, need: int, dev: int, device):
     """(address, bytes) of the caller's workspace, or of a new one of `need` bytes, and the new one."""
     if workspace is None:
@@ -722,7 +729,7 @@ def w8a8_lora_gemm(a, b, scale_a, scale_b, x, lora_a, lora_b, adapter_ids, lora_
     if out is None:
         out = torch.empty(m, n, dtype=bf16 if out_dtype is None else out_dtype, device=a.device)
     L = lib()
-    ws, ws_bytes, hold = _workspace(workspace, L.qk_w8a8_lora_gemm_workspace_size(m, n, k, rank), dev, a.device)
+    ws, ws_bytes, hold = _workspace(workspace, _size("qk_w8a8_lora_gemm_workspace_size", dev, m, n, k, rank), dev, a.device)
     st = L.qk_w8a8_lora_gemm(
         m, n, k, _dense(a, dev, i8, (m, k), "a"), _dense(b, dev, i8, (n, k), "b"),
         _dense(scale_a, dev, f32, (m,), "scale_a"), _dense(scale_b, dev, f32, (n,), "scale_b"), output_scale,
@@ -760,8 +767,8 @@ def w8a8_moe_layer(a, scale_a, topk_ids, topk_weights, w_gate_up, scale_gate_up,
     if out is None:
         out = torch.empty(m, hidden, dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=a.device)
     L = lib()
-    ws, ws_bytes, hold = _workspace(workspace, L.qk_w8a8_moe_layer_workspace_size(m, hidden, inter, experts, topk),
-                                    dev, a.device)
+    need = _size("qk_w8a8_moe_layer_workspace_size", dev, m, hidden, inter, experts, topk)
+    ws, ws_bytes, hold = _workspace(workspace, need, dev, a.device)
     st = L.qk_w8a8_moe_layer(
         m, hidden, inter, experts, topk, _dense(a, dev, i8, (m, hidden), "a"),
         _dense(scale_a, dev, f32, (m,), "scale_a"), _dense(topk_ids, dev, torch.int32, (m, topk), "topk_ids"),
