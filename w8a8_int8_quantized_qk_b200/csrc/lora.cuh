@@ -459,19 +459,25 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(Args p) 
 
 // ---------------------------------------------------------------------------
 // out, longer batches: a CTA walks tiles of 16 tokens in a row at its 256 columns,
-// with the next tile's ids, sums and s in flight while the current one is
-// multiplied and stored, so that it reads and writes without a pause; an
+// with the next tile's ids and s and the next two tiles' sums in flight while the
+// current one is multiplied and stored, so that it reads and writes without a
+// pause (a thread copies the sums it will use itself, asynchronously, to its own
+// places in shared memory: no registers, no barrier); an
 // adapter's rows stay in registers from tile to tile (up to 32 ranks).  Each
 // adapter of a tile is multiplied with all 16 rows, and the rows that use it take
 // its result: by selection, not by multiplying with zero, so that an adapter that
 // holds NaN or infinity reaches no row of another.  (A CTA per tile, each with its
 // own chain of loads, took 43 us for 4096 x 4096 where this takes XX.)
 // ---------------------------------------------------------------------------
+constexpr int kSumTiles = 3;                                // tiles of sums in shared memory
+constexpr int kSumBytes = kTile * 256 * 4;                  // of one tile
+
 template <int RK>  // ranks, rounded up to 16, 32, 64 or 128
 __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Args p) {
   // ranks a thread takes of a step (as two instructions' operands, or one's)
   constexpr int STEP = RK < 32 ? 16 : 32, STEPS = RK / STEP, HALVES = STEP / 16, VEC = STEP / 4;
   constexpr int WORDS = RK / 2, PITCH = WORDS + 4, SV = (kTile * WORDS + kExpandThreads - 1) / kExpandThreads;
+  extern __shared__ __align__(16) uint8_t cs[];  // the sums: [tile][row half, column half][thread][16 bytes]
   __shared__ __align__(16) uint32_t ss[2][3][kTile][PITCH];  // s: [buffer][term][row][pair of ranks]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
   const int tiles = (p.m + kTile - 1) / kTile, col0 = blockIdx.y * 256 + warp * 32, col = col0 + q * 8;
@@ -486,19 +492,30 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Arg
   // what a tile needs, requested a tile ahead
   int id_n = -1;
   float sa_n[2];
-  int4 c_n[2][2];
   float2 s_n[SV];
+  int ahead = blockIdx.x, place = 0;  // the next tile whose sums are requested, and where they go
+  auto request = [&]() {
+    const int r0 = ahead * kTile;
+    const uint32_t dst = smem_addr(cs) + place * kSumBytes + tid * 16;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = r0 + g + h * 8;
+      const bool on = in && ahead < tiles && row < p.m;
+      const int32_t* c = p.c + (on ? static_cast<int64_t>(row) * p.n + col : 0);
+      cp_async16(dst + (2 * h) * kExpandThreads * 16, c, on);
+      cp_async16(dst + (2 * h + 1) * kExpandThreads * 16, on ? c + 4 : c, on);
+    }
+    cp_async_commit();
+    ahead += gridDim.x;
+    place = place + 1 == kSumTiles ? 0 : place + 1;
+  };
   auto fetch = [&](int t) {
     const int r0 = t * kTile;
     id_n = (lane < kTile && t < tiles) ? adapter_of(p, r0 + lane) : -1;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int row = r0 + g + h * 8;
-      const bool on = t < tiles && row < p.m;
-      const int32_t* c = p.c + static_cast<int64_t>(row) * p.n + col;
-      sa_n[h] = on ? __ldg(p.sa + row) : 0.0f;
-      c_n[h][0] = on && in ? *reinterpret_cast<const int4*>(c) : make_int4(0, 0, 0, 0);
-      c_n[h][1] = on && in ? *reinterpret_cast<const int4*>(c + 4) : make_int4(0, 0, 0, 0);
+      sa_n[h] = (t < tiles && row < p.m) ? __ldg(p.sa + row) : 0.0f;
     }
     // (s of tokens without an adapter holds anything: their rows take no product)
 #pragma unroll
@@ -516,14 +533,15 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Arg
       }
     }
   };
+  for (int i = 0; i < kSumTiles - 1; ++i) request();
   fetch(blockIdx.x);
   uint32_t bv[4][VEC / 2];
   int held = -1;  // the adapter whose first ranks are in bv
-  int par = 0;
+  int par = 0, here = 0;
   for (int t = blockIdx.x; t < tiles; t += gridDim.x, par ^= 1) {
     const int id = id_n, r0 = t * kTile;
     const float sa[2] = {sa_n[0], sa_n[1]};
-    const int4 c[2][2] = {{c_n[0][0], c_n[0][1]}, {c_n[1][0], c_n[1][1]}};
+    request();
     const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
     unsigned firsts = __ballot_sync(0xFFFFFFFFu, id >= 0 && (same & ((1u << lane) - 1u)) == 0);
 #pragma unroll
@@ -601,11 +619,14 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Arg
           if (first || (i < 2 ? id0 : id1) == use) add[j][i] = d[j][i];
       first = false;
     }
+    cp_async_wait_but<kSumTiles - 1>();
+    const int4* c = reinterpret_cast<const int4*>(cs + here * kSumBytes) + tid;
+    here = here + 1 == kSumTiles ? 0 : here + 1;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int row = r0 + g + h * 8;
       if (row < p.m && in)
-        store8(p, row, col, c[h][0], c[h][1], sa[h], sw[0], sw[1], (h ? id1 : id0) >= 0,
+        store8(p, row, col, c[2 * h * kExpandThreads], c[(2 * h + 1) * kExpandThreads], sa[h], sw[0], sw[1], (h ? id1 : id0) >= 0,
                add[0][2 * h], add[0][2 * h + 1], add[1][2 * h], add[1][2 * h + 1], add[2][2 * h], add[2][2 * h + 1],
                add[3][2 * h], add[3][2 * h + 1]);
     }
@@ -711,7 +732,15 @@ inline int launch_stream(const Args& a, const int8_t* x, const int8_t* w, const 
   return *err == cudaSuccess ? 0 : 2;
 }
 
-inline cudaError_t launch_expand(const Args& a, int num_sms, cudaStream_t stream) {
+template <int RK>
+inline cudaError_t launch_long(const Args& a, dim3 grid, int dev, cudaStream_t stream) {
+  constexpr size_t bytes = static_cast<size_t>(kSumTiles) * kSumBytes;
+  const cudaError_t e = gemm::set_smem_once(lora_expand_long_kernel<RK>, dev, RK / 16, bytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(lora_expand_long_kernel<RK>, grid, dim3(kExpandThreads), bytes, stream, 1, a);
+}
+
+inline cudaError_t launch_expand(const Args& a, int dev, int num_sms, cudaStream_t stream) {
   if (a.beside) {
     const dim3 grid(most_groups(a.m, a.adapters, true), (a.n + kExpandCols - 1) / kExpandCols);
     return launch_pdl(lora_expand_kernel, grid, dim3(kExpandThreads), expand_smem(a.rank), stream, 1, a);
@@ -720,11 +749,11 @@ inline cudaError_t launch_expand(const Args& a, int num_sms, cudaStream_t stream
   const int tiles = (a.m + kTile - 1) / kTile, cols = (a.n + 255) / 256;
   int x = 2 * num_sms / cols;
   x = x < 1 ? 1 : (x > tiles ? tiles : x);
-  const dim3 grid(x, cols), block(kExpandThreads);
-  if (a.rank <= 16) return launch_pdl(lora_expand_long_kernel<16>, grid, block, 0, stream, 1, a);
-  if (a.rank <= 32) return launch_pdl(lora_expand_long_kernel<32>, grid, block, 0, stream, 1, a);
-  if (a.rank <= 64) return launch_pdl(lora_expand_long_kernel<64>, grid, block, 0, stream, 1, a);
-  return launch_pdl(lora_expand_long_kernel<128>, grid, block, 0, stream, 1, a);
+  const dim3 grid(x, cols);
+  if (a.rank <= 16) return launch_long<16>(a, grid, dev, stream);
+  if (a.rank <= 32) return launch_long<32>(a, grid, dev, stream);
+  if (a.rank <= 64) return launch_long<64>(a, grid, dev, stream);
+  return launch_long<128>(a, grid, dev, stream);
 }
 
 }  // namespace lora

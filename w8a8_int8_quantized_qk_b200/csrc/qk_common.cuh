@@ -448,11 +448,21 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool va
                "l"(reinterpret_cast<uint64_t>(src)), "r"(valid ? 4 : 0)
                : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(valid ? 16 : 0)
+               : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+// all but the N most recently committed groups are complete
+template <int N>
+__device__ __forceinline__ void cp_async_wait_but() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 // all but the most recently committed group are complete
 __device__ __forceinline__ void cp_async_wait_prior() {

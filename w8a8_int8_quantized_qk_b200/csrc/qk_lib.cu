@@ -765,7 +765,7 @@ qk_status qk_w8a8_lora_gemm(int m, int n, int k, const int8_t* a, const int8_t* 
                      out_dtype, l.gemm > 0 ? workspace : nullptr, l.gemm, stream, nullptr, nullptr);
   }
   if (st != QK_OK) return st;
-  return cuda_status(lora::launch_expand(la, dev->sms, s), "adapter expand launch");
+  return cuda_status(lora::launch_expand(la, dev_id, dev->sms, s), "adapter expand launch");
 }
 
 // ---- a MoE layer for a few tokens; the workspace holds the pairs' records, the gate
