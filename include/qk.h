@@ -396,10 +396,11 @@ QK_API qk_status qk_w8a8_moe_gemm(int num_experts, int total_m, int n, int k, in
  * adapter.
  *
  * m, n, k, a, b, scale_a, scale_b, output_scale, out   as qk_w8a8_gemm with
- *                group_k = 0 (out required; n above 16776960: QK_ERR_UNSUPPORTED)
+ *                group_k = 0 (out required; m above 2^20 or n above 16776960:
+ *                QK_ERR_UNSUPPORTED)
  * x              [m, k] x_dtype, dense, 16-B aligned: the tokens before their
  *                quantisation (norm_out of the fused norm, say)
- * num_adapters   >= 1
+ * num_adapters   1 .. 2^20 (more: QK_ERR_UNSUPPORTED)
  * rank           8 .. 128, a multiple of 8 (pad smaller ones with zeros)
  * lora_a         [num_adapters, rank, k] bf16, 16-B aligned
  * lora_b         [num_adapters, n, rank] bf16, 16-B aligned

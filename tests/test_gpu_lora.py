@@ -70,7 +70,8 @@ def plain_rows(p, out, alpha, dt):
     (8, 2056, 512, 128, 9), (9, 1032, 1040, 16, 4), (16, 512, 4096, 40, 16), (17, 264, 272, 8, 5),
     (31, 4096, 512, 32, 40), (33, 1032, 2064, 8, 5), (64, 1024, 1040, 64, 7), (65, 136, 528, 128, 2),
     (128, 2048, 512, 16, 3), (129, 264, 272, 56, 4), (200, 1032, 4096, 16, 6), (300, 4096, 1024, 8, 2),
-    (256, 1024, 14336, 16, 3), (700, 520, 528, 72, 11), (2304, 2304, 512, 16, 4)])
+    (256, 1024, 14336, 16, 3), (700, 520, 528, 72, 11), (2304, 2304, 512, 16, 4),
+    (1024, 264, 272, 8, 1200), (1025, 136, 144, 120, 2), (2500, 264, 144, 32, 70), (3000, 520, 80, 16, 1)])
 @pytest.mark.parametrize("x_dtype,out_dtype", [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32),
                                                (torch.bfloat16, torch.float32)])
 def test_lora(m, n, k, rank, adapters, x_dtype, out_dtype):
@@ -82,7 +83,7 @@ def test_lora(m, n, k, rank, adapters, x_dtype, out_dtype):
     assert qk.device_status() == qk.QK_OK
 
 
-@pytest.mark.parametrize("m", [1, 5, 24, 150])
+@pytest.mark.parametrize("m", [1, 5, 24, 150, 2100])
 @pytest.mark.parametrize("kind", ["none", "one", "each", "outside", "grouped"])
 def test_lora_ids(m, kind):
     adapters = max(m, 3)

@@ -82,6 +82,8 @@ def _lora(m=4, n=16, k=32, a=P16, b=P16, sa=P16, sw=P16, x=P16, xdt=qk.QK_BF16, 
     (dict(k=40), qk.QK_ERR_INVALID_ARG),
     (dict(k=133152), qk.QK_ERR_OVERFLOW_BOUND),
     (dict(n=65535 * 256 + 8), qk.QK_ERR_UNSUPPORTED),
+    (dict(m=(1 << 20) + 1), qk.QK_ERR_UNSUPPORTED),
+    (dict(ad=(1 << 20) + 1), qk.QK_ERR_UNSUPPORTED),
     (dict(rank=0), qk.QK_ERR_INVALID_ARG),
     (dict(rank=12), qk.QK_ERR_INVALID_ARG),
     (dict(rank=136), qk.QK_ERR_INVALID_ARG),

@@ -13,10 +13,12 @@
 // A bf16 value is exact there; a binary32 one (s, and x when it is fp32) enters
 // as three bf16 terms, x = h + m + l, each the rounding of what is left: 24 bits,
 // so a product of 16 of them is as good as one of binary32 values.  The 16 rows
-// are tokens of ONE adapter.  Up to 64 tokens they are gathered from the whole
-// batch, so an adapter is read once however its requests lie; in a longer batch,
-// where a request's tokens lie together, they come from 16 tokens in a row, an
-// adapter present there after another, with the other rows left out.
+// are tokens of ONE adapter, gathered from wherever they lie: from the whole batch
+// up to 64 tokens (every CTA sorts them for itself), from 1024 tokens in a row
+// beyond (a first kernel sorts those).  So an adapter is read for its own tokens
+// only, however requests are mixed, and one that holds NaN or infinity reaches no
+// other's rows.  (Tiles of 16 tokens in a row, an adapter present there after
+// another, took 299 us for 1024 x 4096 x 4096, rank 128, 24 adapters in any order.)
 #pragma once
 
 #include "qk_common.cuh"
@@ -43,9 +45,15 @@ struct Args {
   void* out;
   int out_bf16;
   int beside;                 // the sums are formed before s, and beside it
+  int32_t* units;             // workspace of a longer batch: [chunks, kMaxUnits] records of groups
+  int32_t* counts;            // [chunks]: groups of a chunk
+  int most;                   // groups a chunk can have with these adapters
 };
 
 constexpr int kTile = 16;     // rows of a group
+constexpr int kChunk = 1024;  // tokens sorted together
+constexpr int kMaxUnits = kChunk + kChunk / kTile;  // groups of a chunk, at most
+constexpr int kRecord = 20;   // words of a group's record: the adapter, 16 tokens, 3 unused
 constexpr int kMaxParts = 8;  // K parts of s
 
 __device__ __forceinline__ int adapter_of(const Args& p, int row) {
@@ -80,7 +88,6 @@ __device__ __forceinline__ int nth_bit(unsigned mask, int n) {
 // 16 rows of one adapter (or of none: -1).
 struct Group {
   int use;
-  int more;        // another follows in the CTA's list
   int tok[kTile];  // -1: no token
 };
 
@@ -121,10 +128,7 @@ __device__ __forceinline__ bool gather_unit(const Args& p, int u, bool none, Gro
       uint64_t mask = __shfl_sync(0xFFFFFFFFu, same[h], src);
       const int skip = (u - __shfl_sync(0xFFFFFFFFu, at, src)) * kTile + lane;
       const int use = __shfl_sync(0xFFFFFFFFu, id[h], src);
-      if (lane == 0) {
-        gr.use = use;
-        gr.more = 0;
-      }
+      if (lane == 0) gr.use = use;
       if (lane < kTile) {
         for (int n = 0; n < skip && mask != 0; ++n) mask &= mask - 1ull;
         gr.tok[lane] = mask != 0 ? __ffsll(static_cast<long long>(mask)) - 1 : -1;
@@ -136,41 +140,99 @@ __device__ __forceinline__ bool gather_unit(const Args& p, int u, bool none, Gro
   return found;
 }
 
-// The n-th adapter (or none) among tokens 16 t .. 16 t + 15, by warp 0; the list
-// goes on with n + step.
-__device__ __forceinline__ bool tile_group(const Args& p, int t, int n, int step, bool none, Group& gr) {
-  const int lane = threadIdx.x & 31, row = t * kTile + lane;
-  const int id = (lane < kTile && row < p.m) ? adapter_of(p, row) : -2;
-  const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
-  const unsigned firsts =
-      __ballot_sync(0xFFFFFFFFu, id >= (none ? -1 : 0) && (same & ((1u << lane) - 1u)) == 0);
-  if (n >= __popc(firsts)) return false;
-  const int use = __shfl_sync(0xFFFFFFFFu, id, nth_bit(firsts, n));
-  if (lane == 0) {
-    gr.use = use;
-    gr.more = n + step < __popc(firsts) ? 1 : 0;
-  }
-  if (lane < kTile) gr.tok[lane] = id == use ? row : -1;
-  return true;
-}
-
-// Group n of the CTA, by all threads; false when there is none.
-__device__ __forceinline__ bool next_group(const Args& p, int n, int step, bool none, Group& gr, int& ok) {
-  if (threadIdx.x < 32) {
-    const bool found = p.beside ? (n == 0 && gather_unit(p, blockIdx.x, none, gr))
-                                : tile_group(p, blockIdx.x, n, step, none, gr);
-    if (threadIdx.x == 0) ok = found ? 1 : 0;
+// This CTA's group (blockIdx.x), by all threads; false when there is none.
+__device__ __forceinline__ bool group_of_cta(const Args& p, bool none, Group& gr, int& ok) {
+  const int tid = threadIdx.x;
+  if (p.beside) {
+    if (tid < 32) {
+      const bool found = gather_unit(p, blockIdx.x, none, gr);
+      if (tid == 0) ok = found ? 1 : 0;
+    }
+  } else {
+    const int chunk = blockIdx.x / p.most, u = blockIdx.x - chunk * p.most;
+    const int32_t* rec = p.units + (static_cast<int64_t>(chunk) * kMaxUnits + u) * kRecord;
+    const bool found = u < p.counts[chunk] && (none || rec[0] >= 0);
+    if (tid == 0) {
+      ok = found ? 1 : 0;
+      if (found) gr.use = rec[0];
+    }
+    if (found && tid < kTile) gr.tok[tid] = rec[1 + tid];
   }
   __syncthreads();
   return ok != 0;
 }
 
+// The groups of 1024 tokens, one CTA.  A prompt's tokens lie together: where there
+// are at most as many runs of an adapter's tokens as adapters, 32 at most, each run
+// is taken as it stands.  Else a bitonic sort of (adapter + 1, token) in one word, 32
+// apart through shared memory, nearer ones by shuffles.  Then a token's place in its
+// run gives its group and its row there.
+__global__ void __launch_bounds__(kChunk) lora_units_kernel(Args p) {
+  __shared__ uint32_t buf[kChunk + 1];
+  __shared__ int warp_start[kChunk / 32], warp_units[kChunk / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int i = threadIdx.x, lane = i & 31, warp = i >> 5, row = blockIdx.x * kChunk + i;
+  uint32_t key = row < p.m ? (static_cast<uint32_t>(adapter_of(p, row) + 1) << 10) | static_cast<uint32_t>(i) : 0xFFFFFFFFu;
+  buf[i] = key;
+  __syncthreads();
+  const int runs = __syncthreads_count(i > 0 && row < p.m && (buf[i - 1] >> 10) != (key >> 10)) + 1;
+  for (int k = runs <= min(p.adapters + 1, 32) ? 2 * kChunk : 2; k <= kChunk; k <<= 1) {
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      uint32_t other;
+      if (j >= 32) {
+        __syncthreads();
+        buf[i] = key;
+        __syncthreads();
+        other = buf[i ^ j];
+      } else {
+        other = __shfl_xor_sync(0xFFFFFFFFu, key, j);
+      }
+      const bool smaller = ((i & j) == 0) == ((i & k) == 0);
+      key = smaller ? min(key, other) : max(key, other);
+    }
+  }
+  __syncthreads();
+  buf[i] = key;
+  if (i == 0) buf[kChunk] = 0xFFFFFFFFu;
+  __syncthreads();
+  const bool valid = key != 0xFFFFFFFFu;
+  const uint32_t id = key >> 10;
+  const bool first = valid && (i == 0 || (buf[i - 1] >> 10) != id), last = valid && (buf[i + 1] >> 10) != id;
+  // the run's first token: a running maximum of first tokens' places
+  int start = first ? i : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, start, o);
+    if (lane >= o) start = max(start, v);
+  }
+  if (lane == 31) warp_start[warp] = start;
+  __syncthreads();
+  start = max(start, __reduce_max_sync(0xFFFFFFFFu, lane < warp ? warp_start[lane] : 0));
+  const int pos = i - start, slot = pos & (kTile - 1);
+  const bool opens = valid && slot == 0;
+  const unsigned open = __ballot_sync(0xFFFFFFFFu, opens);
+  if (lane == 0) warp_units[warp] = __popc(open);
+  __syncthreads();
+  const int units = warp_units[lane], before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? units : 0);
+  const int unit = before + __popc(open & ((2u << lane) - 1u)) - 1, all = __reduce_add_sync(0xFFFFFFFFu, units);
+  if (i == 0) p.counts[blockIdx.x] = all;
+  if (valid) {
+    int32_t* rec = p.units + (static_cast<int64_t>(blockIdx.x) * kMaxUnits + unit) * kRecord;
+    if (opens) rec[0] = static_cast<int>(id) - 1;
+    rec[1 + slot] = blockIdx.x * kChunk + static_cast<int>(key & (kChunk - 1));
+    if (last)
+      for (int e = slot + 1; e < kTile; ++e) rec[1 + e] = -1;
+  }
+}
+
 // ---------------------------------------------------------------------------
-// s: one CTA per (group, K part and 64 ranks); its 8 warps deal the part's K in steps of 32 and each multiplies all ranks.  The operands
-// come straight from memory: a dot product may sum K in any order, so thread
-// (g, q) takes elements 8 q .. 8 q + 7 of a step (16 bytes) of token g, of token
-// g + 8 and of the adapter's row, four of them for each of two instructions, in
-// the places (2 q, 2 q + 1) and (2 q + 8, 2 q + 9) those have for it.
+// s: one CTA per (group, K part and 64 ranks); its 8 warps deal the part's K in
+// steps of 32 and each multiplies all ranks.  The operands come straight from
+// memory: a dot product may sum K in any order, so thread (g, q) takes elements
+// 8 q .. 8 q + 7 of a step (16 bytes) of rows g and g + 8 and of the adapter's row,
+// four of them for each of two instructions, in the places (2 q, 2 q + 1) and
+// (2 q + 8, 2 q + 9) those have for it.
 // ---------------------------------------------------------------------------
 constexpr int kShrinkThreads = 256;
 constexpr int kShrinkStep = 32;
@@ -211,81 +273,81 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_kernel(Args p) 
   if (!p.beside) griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
-  for (int n = blockIdx.y; next_group(p, n, gridDim.y, false, gr, ok); n += gridDim.y) {
-    const int use = gr.use, tok0 = gr.tok[g], tok1 = gr.tok[g + 8];
-    const int z = blockIdx.z % p.kparts, rg = blockIdx.z / p.kparts * kRankGroup, ranks = min(p.rank - rg, kRankGroup);
-    const int k0 = z * p.kpart, k1 = min(p.k, k0 + p.kpart);
-    const __nv_bfloat16* a = p.la + (static_cast<int64_t>(use) * p.rank + rg) * p.k;
-    float acc[RT][4];
+  if (!group_of_cta(p, false, gr, ok)) {
+    if (p.beside) griddep_wait();
+    return;
+  }
+  const int use = gr.use, tok0 = gr.tok[g], tok1 = gr.tok[g + 8];
+  const int z = blockIdx.z % p.kparts, rg = blockIdx.z / p.kparts * kRankGroup, ranks = min(p.rank - rg, kRankGroup);
+  const int k0 = z * p.kpart, k1 = min(p.k, k0 + p.kpart);
+  const __nv_bfloat16* a = p.la + (static_cast<int64_t>(use) * p.rank + rg) * p.k;
+  float acc[RT][4];
+#pragma unroll
+  for (int j = 0; j < RT; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
+  // U steps' loads are issued together (ld_nc_v4 and mma_bf16 are volatile: they
+  // keep their order)
+  constexpr int U = RT <= 2 ? 4 : ((RT <= 4 || BF16) ? 2 : 1), ROW = NW * kShrinkStep;
+  for (int k = k0 + warp * kShrinkStep + q * 8; k < k1 + q * 8; k += U * ROW) {
+    uint4 x0[U][XV], x1[U][XV], b[U][RT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int ku = k + u * ROW;
+      const bool in = ku < k1;  // (K is a multiple of 16: the last step may be half one)
+      load_x<BF16>(p.x, static_cast<int64_t>(tok0) * p.k + ku, tok0 >= 0 && in, x0[u]);
+      load_x<BF16>(p.x, static_cast<int64_t>(tok1) * p.k + ku, tok1 >= 0 && in, x1[u]);
+#pragma unroll
+      for (int j = 0; j < RT; ++j)
+        b[u][j] = (j * 8 < ranks && in) ? ld_nc_v4(a + static_cast<int64_t>(j * 8 + g) * p.k + ku)
+                                        : make_uint4(0, 0, 0, 0);
+    }
+    // The instruction truncates as it accumulates: a batch's products are summed on
+    // their own, the smallest terms first, and added to the rest with rounding (a
+    // single chain over 8192 values of K was 7e-7 off, relative, this is 1.4e-7).
+    float part[RT][4];
 #pragma unroll
     for (int j = 0; j < RT; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-    // U steps' loads are issued together (ld_nc_v4 and mma_bf16 are volatile: they
-    // keep their order)
-    constexpr int U = RT <= 2 ? 4 : ((RT <= 4 || BF16) ? 2 : 1), ROW = NW * kShrinkStep;
-    for (int k = k0 + warp * kShrinkStep + q * 8; k < k1 + q * 8; k += U * ROW) {
-      uint4 x0[U][XV], x1[U][XV], b[U][RT];
+      for (int i = 0; i < 4; ++i) part[j][i] = 0.0f;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int ku = k + u * ROW;
-        const bool in = ku < k1;  // (K is a multiple of 16: the last step may be half one)
-        load_x<BF16>(p.x, static_cast<int64_t>(tok0) * p.k + ku, tok0 >= 0 && in, x0[u]);
-        load_x<BF16>(p.x, static_cast<int64_t>(tok1) * p.k + ku, tok1 >= 0 && in, x1[u]);
+    for (int u = 0; u < U; ++u) {
+      uint32_t t0[4][TERMS], t1[4][TERMS];
+      terms_x<BF16>(x0[u], t0);
+      terms_x<BF16>(x1[u], t1);
 #pragma unroll
-        for (int j = 0; j < RT; ++j)
-          b[u][j] = (j * 8 < ranks && in) ? ld_nc_v4(a + static_cast<int64_t>(j * 8 + g) * p.k + ku)
-                                          : make_uint4(0, 0, 0, 0);
-      }
-      // The instruction truncates as it accumulates: a batch's products are summed on
-      // their own, the smallest terms first, and added to the rest with rounding (a
-      // single chain over 8192 values of K was 7e-7 off, relative, this is 1.4e-7).
-      float part[RT][4];
+      for (int i = TERMS - 1; i >= 0; --i) {
+        const uint32_t f0[4] = {t0[0][i], t1[0][i], t0[1][i], t1[1][i]};
+        const uint32_t f1[4] = {t0[2][i], t1[2][i], t0[3][i], t1[3][i]};
 #pragma unroll
-      for (int j = 0; j < RT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) part[j][i] = 0.0f;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        uint32_t t0[4][TERMS], t1[4][TERMS];
-        terms_x<BF16>(x0[u], t0);
-        terms_x<BF16>(x1[u], t1);
-#pragma unroll
-        for (int i = TERMS - 1; i >= 0; --i) {
-          const uint32_t f0[4] = {t0[0][i], t1[0][i], t0[1][i], t1[1][i]};
-          const uint32_t f1[4] = {t0[2][i], t1[2][i], t0[3][i], t1[3][i]};
-#pragma unroll
-          for (int j = 0; j < RT; ++j) {
-            mma_bf16(part[j], f0, b[u][j].x, b[u][j].y);
-            mma_bf16(part[j], f1, b[u][j].z, b[u][j].w);
-          }
+        for (int j = 0; j < RT; ++j) {
+          mma_bf16(part[j], f0, b[u][j].x, b[u][j].y);
+          mma_bf16(part[j], f1, b[u][j].z, b[u][j].w);
         }
       }
-#pragma unroll
-      for (int j = 0; j < RT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][i] = __fadd_rn(acc[j][i], part[j][i]);
     }
 #pragma unroll
-    for (int j = 0; j < RT; ++j) {
-      red[warp][g][j * 8 + 2 * q] = acc[j][0];
-      red[warp][g][j * 8 + 2 * q + 1] = acc[j][1];
-      red[warp][g + 8][j * 8 + 2 * q] = acc[j][2];
-      red[warp][g + 8][j * 8 + 2 * q + 1] = acc[j][3];
-    }
-    __syncthreads();
-    const float ls = p.lscale ? __ldg(p.lscale + use) : 1.0f;
-    float* s = p.s + static_cast<int64_t>(z) * p.m * p.rank + rg;
-    for (int i = tid; i < kTile * ranks; i += kShrinkThreads) {
-      const int row = i / ranks, r = i - row * ranks;
-      if (gr.tok[row] < 0) continue;
-      float v = 0.0f;
+    for (int j = 0; j < RT; ++j)
 #pragma unroll
-      for (int w = 0; w < NW; ++w) v += red[w][row][r];
-      s[static_cast<int64_t>(gr.tok[row]) * p.rank + r] = ls * v;
-    }
-    if (!gr.more) break;
-    __syncthreads();  // the group and the sums are rewritten
+      for (int i = 0; i < 4; ++i) acc[j][i] = __fadd_rn(acc[j][i], part[j][i]);
+  }
+#pragma unroll
+  for (int j = 0; j < RT; ++j) {
+    red[warp][g][j * 8 + 2 * q] = acc[j][0];
+    red[warp][g][j * 8 + 2 * q + 1] = acc[j][1];
+    red[warp][g + 8][j * 8 + 2 * q] = acc[j][2];
+    red[warp][g + 8][j * 8 + 2 * q + 1] = acc[j][3];
+  }
+  __syncthreads();
+  const float ls = p.lscale ? __ldg(p.lscale + use) : 1.0f;
+  float* s = p.s + static_cast<int64_t>(z) * p.m * p.rank + rg;
+  for (int i = tid; i < kTile * ranks; i += kShrinkThreads) {
+    const int row = i / ranks, r = i - row * ranks;
+    if (gr.tok[row] < 0) continue;
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) v += red[w][row][r];
+    s[static_cast<int64_t>(gr.tok[row]) * p.rank + r] = ls * v;
   }
   if (p.beside) griddep_wait();
 }
@@ -343,7 +405,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(Args p) 
     sw[v][0] = in ? __ldg(reinterpret_cast<const float4*>(p.sw + col)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     sw[v][1] = in ? __ldg(reinterpret_cast<const float4*>(p.sw + col) + 1) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   }
-  if (!next_group(p, 0, 1, true, gr, ok)) {
+  if (!group_of_cta(p, true, gr, ok)) {
     griddep_wait();
     return;
   }
@@ -458,125 +520,159 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(Args p) 
 }
 
 // ---------------------------------------------------------------------------
-// out, longer batches: a CTA walks tiles of 16 tokens in a row at its 256 columns,
-// with the next tile's ids and s and the next two tiles' sums in flight while the
-// current one is multiplied and stored, so that it reads and writes without a
-// pause (a thread copies the sums it will use itself, asynchronously, to its own
-// places in shared memory: no registers, no barrier); an
-// adapter's rows stay in registers from tile to tile (up to 32 ranks).  Each
-// adapter of a tile is multiplied with all 16 rows, and the rows that use it take
-// its result: by selection, not by multiplying with zero, so that an adapter that
-// holds NaN or infinity reaches no row of another.  (A CTA per tile, each with its
-// own chain of loads, took 43 us for 4096 x 4096 where this takes XX.)
+// out, longer batches: a CTA walks its share of the groups, in order, at its 256
+// columns, with the next group's s and the next two groups' sums in flight while
+// the current one is multiplied and stored, so that it reads and writes without a
+// pause.  (A warp copies the sums it will use itself, asynchronously, eight lanes a
+// row so that each fetches whole sectors: no registers, no barrier of the CTA.)  Consecutive groups mostly
+// share their adapter, whose rows stay where they are until it changes: in
+// registers up to 32 ranks, in a thread's own places in shared memory beyond.
 // ---------------------------------------------------------------------------
-constexpr int kSumTiles = 3;                                // tiles of sums in shared memory
-constexpr int kSumBytes = kTile * 256 * 4;                  // of one tile
+constexpr int kSumTiles = 3;                // groups' sums in shared memory
+constexpr int kSumBytes = kTile * 256 * 4;  // of one group
+constexpr int kRecords = 8, kRecordsAhead = 5;
+
+template <int RK>
+constexpr size_t long_smem() {
+  return static_cast<size_t>(kSumTiles) * kSumBytes + (RK > 32 ? kExpandThreads * RK * 2 : 0);
+}
 
 template <int RK>  // ranks, rounded up to 16, 32, 64 or 128
 __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Args p) {
   // ranks a thread takes of a step (as two instructions' operands, or one's)
   constexpr int STEP = RK < 32 ? 16 : 32, STEPS = RK / STEP, HALVES = STEP / 16, VEC = STEP / 4;
   constexpr int WORDS = RK / 2, PITCH = WORDS + 4, SV = (kTile * WORDS + kExpandThreads - 1) / kExpandThreads;
-  extern __shared__ __align__(16) uint8_t cs[];  // the sums: [tile][row half, column half][thread][16 bytes]
+  // the sums: [group][warp][row][8 pieces of 16 bytes, a pair exchanged in odd rows];
+  // the adapter's rows: [step][product][thread][16 bytes]
+  extern __shared__ __align__(16) uint8_t cs[];
   __shared__ __align__(16) uint32_t ss[2][3][kTile][PITCH];  // s: [buffer][term][row][pair of ranks]
+  __shared__ __align__(16) int recs[kRecords][kRecord];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
-  const int tiles = (p.m + kTile - 1) / kTile, col0 = blockIdx.y * 256 + warp * 32, col = col0 + q * 8;
+  const int col0 = blockIdx.y * 256 + warp * 32, col = col0 + q * 8;
   const bool in = col < p.n;  // (n is a multiple of 8)
   float4 sw[2] = {};
   if (in) {
     sw[0] = __ldg(reinterpret_cast<const float4*>(p.sw + col));
     sw[1] = __ldg(reinterpret_cast<const float4*>(p.sw + col) + 1);
   }
-  griddep_wait();
-  griddep_launch_dependents();
-  // what a tile needs, requested a tile ahead
-  int id_n = -1;
+  // (every kernel from the groups to the product lets the next one start only after
+  // its own wait: groups and s are complete, only the sums are not)
+  // this CTA's groups: [walk, end) of all chunks' together
+  const int chunks = (p.m + kChunk - 1) / kChunk;
+  int total = 0;
+  for (int c = 0; c < chunks; ++c) total += __ldg(p.counts + c);
+  int walk = static_cast<int>(static_cast<int64_t>(total) * blockIdx.x / gridDim.x);
+  const int end = static_cast<int>(static_cast<int64_t>(total) * (blockIdx.x + 1) / gridDim.x), mine = end - walk;
+  if (mine == 0) {
+    griddep_wait();
+    return;
+  }
+  int chunk = 0, base = 0, count = __ldg(p.counts);
+  auto record = [&](int i) {  // requests the record of this CTA's group i (they are asked for in order)
+    if (walk >= end) return;
+    while (walk - base >= count) {
+      base += count;
+      count = __ldg(p.counts + ++chunk);
+    }
+    const int32_t* src = p.units + (static_cast<int64_t>(chunk) * kMaxUnits + walk - base) * kRecord;
+    if (tid < kRecord / 4) cp_async16(smem_addr(&recs[i % kRecords][tid * 4]), src + tid * 4, true);
+    ++walk;
+  };
+  auto sums = [&](int i) {  // requests the sums of group i
+    const int* rec = recs[i % kRecords];
+    const int r0 = lane >> 3, piece = lane & 7, cc = col0 + piece * 4;
+    const uint32_t dst = smem_addr(cs) + (i % kSumTiles) * kSumBytes + warp * (kTile * 128) + r0 * 128 +
+                         (piece ^ (r0 & 1)) * 16;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const int tok = i < mine ? rec[1 + r0 + h * 4] : -1;
+      const bool on = cc < p.n && tok >= 0;
+      cp_async16(dst + h * 512, p.c + (on ? static_cast<int64_t>(tok) * p.n + cc : 0), on);
+    }
+  };
   float sa_n[2];
   float2 s_n[SV];
-  int ahead = blockIdx.x, place = 0;  // the next tile whose sums are requested, and where they go
-  auto request = [&]() {
-    const int r0 = ahead * kTile;
-    const uint32_t dst = smem_addr(cs) + place * kSumBytes + tid * 16;
+  auto fetch = [&](int i) {  // s and the tokens' scales of group i
+    if (i >= mine) return;
+    const int* rec = recs[i % kRecords];
+    const bool has = rec[0] >= 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int row = r0 + g + h * 8;
-      const bool on = in && ahead < tiles && row < p.m;
-      const int32_t* c = p.c + (on ? static_cast<int64_t>(row) * p.n + col : 0);
-      cp_async16(dst + (2 * h) * kExpandThreads * 16, c, on);
-      cp_async16(dst + (2 * h + 1) * kExpandThreads * 16, on ? c + 4 : c, on);
+      const int tok = rec[1 + g + h * 8];
+      sa_n[h] = tok >= 0 ? __ldg(p.sa + tok) : 0.0f;
     }
-    cp_async_commit();
-    ahead += gridDim.x;
-    place = place + 1 == kSumTiles ? 0 : place + 1;
-  };
-  auto fetch = [&](int t) {
-    const int r0 = t * kTile;
-    id_n = (lane < kTile && t < tiles) ? adapter_of(p, r0 + lane) : -1;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = r0 + g + h * 8;
-      sa_n[h] = (t < tiles && row < p.m) ? __ldg(p.sa + row) : 0.0f;
-    }
-    // (s of tokens without an adapter holds anything: their rows take no product)
-#pragma unroll
-    for (int i = 0; i < SV; ++i) {
-      const int at = tid + i * kExpandThreads, row = at / WORDS, r = 2 * (at % WORDS);
-      s_n[i] = make_float2(0.0f, 0.0f);
-      if (row < kTile && r < p.rank && t < tiles && r0 + row < p.m) {
-        const float* s = p.s + static_cast<int64_t>(r0 + row) * p.rank + r;
-        s_n[i] = *reinterpret_cast<const float2*>(s);
-        for (int z = 1; z < p.kparts; ++z) {
-          const float2 f = *reinterpret_cast<const float2*>(s + static_cast<int64_t>(z) * p.m * p.rank);
-          s_n[i].x += f.x;
-          s_n[i].y += f.y;
+    for (int v = 0; v < SV; ++v) {
+      const int at = tid + v * kExpandThreads, row = at / WORDS, r = 2 * (at % WORDS);
+      s_n[v] = make_float2(0.0f, 0.0f);
+      if (row < kTile && r < p.rank && has) {
+        const int tok = rec[1 + row];
+        if (tok >= 0) {
+          const float* s = p.s + static_cast<int64_t>(tok) * p.rank + r;
+          s_n[v] = *reinterpret_cast<const float2*>(s);
+          for (int z = 1; z < p.kparts; ++z) {
+            const float2 f = *reinterpret_cast<const float2*>(s + static_cast<int64_t>(z) * p.m * p.rank);
+            s_n[v].x += f.x;
+            s_n[v].y += f.y;
+          }
         }
       }
     }
   };
-  for (int i = 0; i < kSumTiles - 1; ++i) request();
-  fetch(blockIdx.x);
+  for (int i = 0; i < kRecordsAhead; ++i) record(i);
+  cp_async_commit();
+  cp_async_wait_all();
+  __syncthreads();
+  fetch(0);
+  griddep_wait();
+  griddep_launch_dependents();
+  for (int i = 0; i < kSumTiles - 1; ++i) {
+    sums(i);
+    cp_async_commit();
+  }
   uint32_t bv[4][VEC / 2];
-  int held = -1;  // the adapter whose first ranks are in bv
-  int par = 0, here = 0;
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x, par ^= 1) {
-    const int id = id_n, r0 = t * kTile;
+  int held = -1;  // the adapter whose rows are held
+  for (int i = 0; i < mine; ++i) {
+    const int* rec = recs[i % kRecords];
+    const int use = rec[0], par = i & 1;
     const float sa[2] = {sa_n[0], sa_n[1]};
-    request();
-    const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
-    unsigned firsts = __ballot_sync(0xFFFFFFFFu, id >= 0 && (same & ((1u << lane) - 1u)) == 0);
+    if (use >= 0) {
 #pragma unroll
-    for (int i = 0; i < SV; ++i) {
-      const int at = tid + i * kExpandThreads;
-      if (at < kTile * WORDS) {
-        uint32_t term[3];
-        split3(s_n[i].x, s_n[i].y, term);
+      for (int v = 0; v < SV; ++v) {
+        const int at = tid + v * kExpandThreads;
+        if (at < kTile * WORDS) {
+          uint32_t term[3];
+          split3(s_n[v].x, s_n[v].y, term);
 #pragma unroll
-        for (int e = 0; e < 3; ++e) ss[par][e][at / WORDS][at % WORDS] = term[e];
+          for (int e = 0; e < 3; ++e) ss[par][e][at / WORDS][at % WORDS] = term[e];
+        }
       }
     }
-    fetch(t + gridDim.x);
+    // (s and the records that were waited for below are there for every thread)
     __syncthreads();
-    const int id0 = __shfl_sync(0xFFFFFFFFu, id, g), id1 = __shfl_sync(0xFFFFFFFFu, id, g + 8);
-    float add[4][4];
-    bool first = true;
-    while (firsts != 0) {
-      const int use = __shfl_sync(0xFFFFFFFFu, id, __ffs(firsts) - 1);
-      firsts &= firsts - 1u;
-      const __nv_bfloat16* b = p.lb + static_cast<int64_t>(use) * p.n * p.rank;
-      float d[4][4];
+    sums(i + kSumTiles - 1);
+    record(i + kRecordsAhead);
+    cp_async_commit();
+    fetch(i + 1);
+    float d[4][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[j][i] = 0.0f;
+      for (int e = 0; e < 4; ++e) d[j][e] = 0.0f;
+    if (use >= 0) {
+      uint8_t* bs = cs + kSumTiles * kSumBytes + tid * 16;
+      if (held != use) {
+        const __nv_bfloat16* b = p.lb + static_cast<int64_t>(use) * p.n * p.rank;
 #pragma unroll
-      for (int st = 0; st < STEPS; ++st) {
-        if (STEPS > 1 || held != use) {
+        for (int st = 0; st < STEPS; ++st)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int r = st * STEP + q * VEC, cb = col0 + (g >> 1) * 8 + j * 2 + (g & 1);
             const bool on = cb < p.n && r < p.rank;
-            const __nv_bfloat16* at = b + static_cast<int64_t>(cb) * p.rank + r;
-            if constexpr (HALVES == 2) {
+            const __nv_bfloat16* at = on ? b + static_cast<int64_t>(cb) * p.rank + r : b;
+            if constexpr (RK > 32) {
+              cp_async16(smem_addr(bs) + (st * 4 + j) * kExpandThreads * 16, at, on);
+            } else if constexpr (HALVES == 2) {
               const uint4 v = on ? __ldg(reinterpret_cast<const uint4*>(at)) : make_uint4(0, 0, 0, 0);
               bv[j][0] = v.x;
               bv[j][1] = v.y;
@@ -588,6 +684,23 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Arg
               bv[j][1] = v.y;
             }
           }
+        if constexpr (RK > 32) {
+          cp_async_commit();
+          cp_async_wait_all();
+        }
+        held = use;
+      }
+#pragma unroll
+      for (int st = 0; st < STEPS; ++st) {
+        if constexpr (RK > 32) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 v = *reinterpret_cast<const uint4*>(bs + (st * 4 + j) * kExpandThreads * 16);
+            bv[j][0] = v.x;
+            bv[j][1] = v.y;
+            bv[j][2] = v.z;
+            bv[j][3] = v.w;
+          }
         }
 #pragma unroll
         for (int e = 2; e >= 0; --e) {  // the smallest terms first
@@ -595,11 +708,13 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Arg
           const uint32_t* a0 = &ss[par][e][g][st * (STEP / 2) + q * (VEC / 2)];
           const uint32_t* a1 = &ss[par][e][g + 8][st * (STEP / 2) + q * (VEC / 2)];
           if constexpr (HALVES == 2) {
-            *reinterpret_cast<uint4*>(x0) = *reinterpret_cast<const uint4*>(a0);
-            *reinterpret_cast<uint4*>(x1) = *reinterpret_cast<const uint4*>(a1);
+            const uint4 v0 = *reinterpret_cast<const uint4*>(a0), v1 = *reinterpret_cast<const uint4*>(a1);
+            x0[0] = v0.x, x0[1] = v0.y, x0[2] = v0.z, x0[3] = v0.w;
+            x1[0] = v1.x, x1[1] = v1.y, x1[2] = v1.z, x1[3] = v1.w;
           } else {
-            *reinterpret_cast<uint2*>(x0) = *reinterpret_cast<const uint2*>(a0);
-            *reinterpret_cast<uint2*>(x1) = *reinterpret_cast<const uint2*>(a1);
+            const uint2 v0 = *reinterpret_cast<const uint2*>(a0), v1 = *reinterpret_cast<const uint2*>(a1);
+            x0[0] = v0.x, x0[1] = v0.y;
+            x1[0] = v1.x, x1[1] = v1.y;
           }
 #pragma unroll
           for (int h = 0; h < HALVES; ++h) {
@@ -609,26 +724,19 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Arg
           }
         }
       }
-      held = use;
-      // (the first adapter's result goes to every row: rows of another are overwritten
-      // by theirs, rows without one do not take it)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (first || (i < 2 ? id0 : id1) == use) add[j][i] = d[j][i];
-      first = false;
     }
     cp_async_wait_but<kSumTiles - 1>();
-    const int4* c = reinterpret_cast<const int4*>(cs + here * kSumBytes) + tid;
-    here = here + 1 == kSumTiles ? 0 : here + 1;
+    __syncwarp();  // (the warp's lanes copied them for one another)
+    const uint8_t* c = cs + (i % kSumTiles) * kSumBytes + warp * (kTile * 128) + g * 128;
+    const int e0 = ((2 * q) ^ (g & 1)) * 16, e1 = ((2 * q + 1) ^ (g & 1)) * 16;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int row = r0 + g + h * 8;
-      if (row < p.m && in)
-        store8(p, row, col, c[2 * h * kExpandThreads], c[(2 * h + 1) * kExpandThreads], sa[h], sw[0], sw[1], (h ? id1 : id0) >= 0,
-               add[0][2 * h], add[0][2 * h + 1], add[1][2 * h], add[1][2 * h + 1], add[2][2 * h], add[2][2 * h + 1],
-               add[3][2 * h], add[3][2 * h + 1]);
+      const int tok = rec[1 + g + h * 8];
+      if (tok >= 0 && in)
+        store8(p, tok, col, *reinterpret_cast<const int4*>(c + h * 1024 + e0),
+               *reinterpret_cast<const int4*>(c + h * 1024 + e1), sa[h], sw[0], sw[1], use >= 0,
+               d[0][2 * h], d[0][2 * h + 1], d[1][2 * h], d[1][2 * h + 1], d[2][2 * h], d[2][2 * h + 1], d[3][2 * h],
+               d[3][2 * h + 1]);
     }
   }
 }
@@ -676,18 +784,19 @@ inline stream::Plan stream_plan(int m, int n, int k, int num_sms) {
   return stream::plan(m, n, k, num_sms, kSlices - 1, kRing);
 }
 
-// Groups at most: of the whole batch (gathered; a token without an adapter is in
-// none or, for the output, in one more), or of a tile.
-inline int most_groups(int m, int adapters, bool none) {
+inline int chunks_of(int m) { return (m + kChunk - 1) / kChunk; }
+
+// Groups at most of `tokens` sorted together (those without an adapter make groups
+// of their own, for the output): every adapter's last one may be partly filled.
+inline int most_groups(int tokens, int adapters, bool none) {
   const int a = adapters + (none ? 1 : 0);
-  if (streams(m)) return (a < m ? a : m) + m / kTile;
-  return a < kTile ? a : kTile;
+  return (a < tokens ? a : tokens) + tokens / kTile;
 }
 
-// K parts of s: as many as keep its CTAs (in a long batch a tile's one or two
-// groups) within one an SM, no part under 512.  `adapters` 1 gives the most parts.
+// K parts of s: as many as keep its CTAs within one an SM, no part under 512.
+// `adapters` 1 gives the most parts.
 inline int shrink_parts(int m, int k, int adapters, int num_sms) {
-  const int ctas = streams(m) ? most_groups(m, adapters, false) : (m + kTile - 1) / kTile * 2;
+  const int ctas = streams(m) ? most_groups(m, adapters, false) : (m + kTile - 1) / kTile;
   int parts = 1;
   while (parts < kMaxParts && 2 * ctas * parts <= num_sms && k / (2 * parts) >= 512) parts *= 2;
   return parts;
@@ -703,21 +812,20 @@ inline cudaError_t launch_shrink_rt(const Args& a, dim3 grid, int dev, cudaStrea
 }
 
 template <bool BF16>
-inline cudaError_t launch_shrink_t(const Args& a, int dev, int num_sms, cudaStream_t stream) {
-  const int most = most_groups(a.m, a.adapters, false), rgroups = (a.rank + kRankGroup - 1) / kRankGroup;
-  const int tiles = (a.m + kTile - 1) / kTile;
-  int y = a.beside ? 1 : 4 * num_sms / (tiles * a.kparts * rgroups);
-  y = y < 1 ? 1 : (y > most ? most : y);
-  const dim3 grid(a.beside ? most : tiles, y, a.kparts * rgroups);
+inline cudaError_t launch_shrink_t(const Args& a, int dev, cudaStream_t stream) {
+  const int groups = a.beside ? most_groups(a.m, a.adapters, false) : chunks_of(a.m) * a.most;
+  const dim3 grid(groups, 1, a.kparts * ((a.rank + kRankGroup - 1) / kRankGroup));
   if (a.rank <= 16) return launch_shrink_rt<BF16, 2>(a, grid, dev, stream);
   if (a.rank <= 32) return launch_shrink_rt<BF16, 4>(a, grid, dev, stream);
   return launch_shrink_rt<BF16, 8>(a, grid, dev, stream);
 }
 
-// A long batch's tiles take their groups one after another, unless the grid is
-// small enough for CTAs of their own (four an SM).
-inline cudaError_t launch_shrink(const Args& a, bool x_bf16, int dev, int num_sms, cudaStream_t stream) {
-  return x_bf16 ? launch_shrink_t<true>(a, dev, num_sms, stream) : launch_shrink_t<false>(a, dev, num_sms, stream);
+inline cudaError_t launch_shrink(const Args& a, bool x_bf16, int dev, cudaStream_t stream) {
+  return x_bf16 ? launch_shrink_t<true>(a, dev, stream) : launch_shrink_t<false>(a, dev, stream);
+}
+
+inline cudaError_t launch_units(const Args& a, cudaStream_t stream) {
+  return launch_pdl(lora_units_kernel, dim3(chunks_of(a.m)), dim3(kChunk), 0, stream, 1, a);
 }
 
 // Returns 0, 1 when a tensor map could not be made, 2 with *err set.
@@ -734,7 +842,7 @@ inline int launch_stream(const Args& a, const int8_t* x, const int8_t* w, const 
 
 template <int RK>
 inline cudaError_t launch_long(const Args& a, dim3 grid, int dev, cudaStream_t stream) {
-  constexpr size_t bytes = static_cast<size_t>(kSumTiles) * kSumBytes;
+  constexpr size_t bytes = long_smem<RK>();
   const cudaError_t e = gemm::set_smem_once(lora_expand_long_kernel<RK>, dev, RK / 16, bytes);
   if (e != cudaSuccess) return e;
   return launch_pdl(lora_expand_long_kernel<RK>, grid, dim3(kExpandThreads), bytes, stream, 1, a);
@@ -745,10 +853,11 @@ inline cudaError_t launch_expand(const Args& a, int dev, int num_sms, cudaStream
     const dim3 grid(most_groups(a.m, a.adapters, true), (a.n + kExpandCols - 1) / kExpandCols);
     return launch_pdl(lora_expand_kernel, grid, dim3(kExpandThreads), expand_smem(a.rank), stream, 1, a);
   }
-  // as many CTAs as are resident at once (two an SM), at least one a column block
-  const int tiles = (a.m + kTile - 1) / kTile, cols = (a.n + 255) / 256;
-  int x = 2 * num_sms / cols;
-  x = x < 1 ? 1 : (x > tiles ? tiles : x);
+  // as many CTAs as are resident at once (two an SM, one at 128 ranks), at least one
+  // a column block
+  const int most = chunks_of(a.m) * a.most, cols = (a.n + 255) / 256;
+  int x = (a.rank <= 64 ? 2 : 1) * num_sms / cols;
+  x = x < 1 ? 1 : (x > most ? most : x);
   const dim3 grid(x, cols);
   if (a.rank <= 16) return launch_long<16>(a, grid, dev, stream);
   if (a.rank <= 32) return launch_long<32>(a, grid, dev, stream);

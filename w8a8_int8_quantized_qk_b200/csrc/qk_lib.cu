@@ -662,31 +662,36 @@ size_t qk_w8a8_linear_workspace_size(int m, int n, int k, int group_k) {
 }
 
 // ---- adapters beside the projection; the workspace holds the GEMM's own part,
-// then s [parts, m, rank], then the int32 sums [slices, m, n]
+// then the groups of a longer batch, then s [parts, m, rank], then the int32 sums
+// [slices, m, n]
 namespace {
 struct LoraLayout {
-  size_t gemm, s, c, total;
+  size_t gemm, units, counts, s, c, total;  // sizes
 };
 
 LoraLayout lora_layout(int m, int n, int k, int rank, int num_sms) {
   LoraLayout l;
   const bool small = lora::streams(m);
   l.gemm = small ? 0 : round256(qk_w8a8_gemm_workspace_size(m, n, k, 0));
+  l.units = small ? 0 : round256(static_cast<size_t>(lora::chunks_of(m)) * lora::kMaxUnits * lora::kRecord * 4);
+  l.counts = small ? 0 : round256(static_cast<size_t>(lora::chunks_of(m)) * 4);
   l.s = round256(static_cast<size_t>(lora::shrink_parts(m, k, 1, num_sms)) * m * rank * 4);
   l.c = round256(static_cast<size_t>(small ? lora::stream_plan(m, n, k, num_sms).max_slices : 1) * m *
                  static_cast<size_t>(n) * 4);
-  l.total = l.gemm + l.s + l.c;
+  l.total = l.gemm + l.units + l.counts + l.s + l.c;
   return l;
 }
 
 // (blocks of 256 columns are a grid's second dimension)
-constexpr int kLoraMaxN = 65535 * 256;
+constexpr int kLoraMaxN = 65535 * 256, kLoraMaxM = 1 << 20;
+// (an adapter and a place among 1024 tokens share a word)
+constexpr int kLoraMaxAdapters = 1 << 20;
 
 qk_status lora_check(int m, int n, int k, int rank) {
   const qk_status st = gemm_check(m, n, k, 0);
   if (st != QK_OK) return st;
   if (rank < 8 || rank > 128 || (rank % 8) != 0) return QK_ERR_INVALID_ARG;
-  return n > kLoraMaxN ? QK_ERR_UNSUPPORTED : QK_OK;
+  return (n > kLoraMaxN || m > kLoraMaxM) ? QK_ERR_UNSUPPORTED : QK_OK;
 }
 }  // namespace
 
@@ -704,6 +709,7 @@ qk_status qk_w8a8_lora_gemm(int m, int n, int k, const int8_t* a, const int8_t* 
   qk_status st = lora_check(m, n, k, rank);
   if (st != QK_OK) return st;
   if (num_adapters < 1) return QK_ERR_INVALID_ARG;
+  if (num_adapters > kLoraMaxAdapters) return QK_ERR_UNSUPPORTED;
   if (x_dtype != QK_F32 && x_dtype != QK_BF16) return QK_ERR_INVALID_ARG;
   if (out_dtype != QK_F32 && out_dtype != QK_BF16) return QK_ERR_INVALID_ARG;
   if (m == 0 || n == 0) return QK_OK;
@@ -735,8 +741,13 @@ qk_status qk_w8a8_lora_gemm(int m, int n, int k, const int8_t* a, const int8_t* 
   la.sa = scale_a;
   la.sw = scale_b;
   la.alpha = output_scale;
-  la.s = reinterpret_cast<float*>(ws + l.gemm);
-  la.c = reinterpret_cast<const int32_t*>(ws + l.gemm + l.s);
+  ws += l.gemm;
+  la.units = reinterpret_cast<int32_t*>(ws);
+  la.counts = reinterpret_cast<int32_t*>(ws + l.units);
+  ws += l.units + l.counts;
+  la.s = reinterpret_cast<float*>(ws);
+  la.c = reinterpret_cast<const int32_t*>(ws + l.s);
+  la.most = lora::most_groups(lora::kChunk, num_adapters, true);
   la.out = out;
   la.out_bf16 = out_dtype == QK_BF16;
   la.kparts = lora::shrink_parts(m, k, num_adapters, dev->sms);
@@ -752,14 +763,16 @@ qk_status qk_w8a8_lora_gemm(int m, int n, int k, const int8_t* a, const int8_t* 
     const int r = lora::launch_stream(la, a, b, sp, dev_id, dev->sms, s, &e);
     st = r == 1 ? cuda_status(cudaErrorInvalidValue, "tensor map encoding") : cuda_status(e, "projection launch");
     if (st != QK_OK) return st;
-    st = cuda_status(lora::launch_shrink(la, x_dtype == QK_BF16, dev_id, dev->sms, s), "adapter shrink launch");
+    st = cuda_status(lora::launch_shrink(la, x_dtype == QK_BF16, dev_id, s), "adapter shrink launch");
   } else {
     // the GEMM's counters and split-K accumulators start at zero
     gemm::PairPlan pl;
     if (l.gemm > 0 && pair_plan_for(m, n, k, 0, &pl) &&
         cudaMemsetAsync(workspace, 0, gemm::pair_workspace_zero_bytes(pl), s) != cudaSuccess)
       return QK_ERR_CUDA;
-    st = cuda_status(lora::launch_shrink(la, x_dtype == QK_BF16, dev_id, dev->sms, s), "adapter shrink launch");
+    st = cuda_status(lora::launch_units(la, s), "adapter groups launch");
+    if (st != QK_OK) return st;
+    st = cuda_status(lora::launch_shrink(la, x_dtype == QK_BF16, dev_id, s), "adapter shrink launch");
     if (st != QK_OK) return st;
     st = gemm_common(m, n, k, a, b, scale_a, scale_b, 0, output_scale, const_cast<int32_t*>(la.c), nullptr,
                      out_dtype, l.gemm > 0 ? workspace : nullptr, l.gemm, stream, nullptr, nullptr);
