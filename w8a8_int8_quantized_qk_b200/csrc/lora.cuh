@@ -378,7 +378,7 @@ __device__ __forceinline__ void store8(const Args& p, int row, int col, const in
   };
   const float v0 = val(c0.x, w0.x, d0), v1 = val(c0.y, w0.y, d1), v2 = val(c0.z, w0.z, d2), v3 = val(c0.w, w0.w, d3);
   const float v4 = val(c1.x, w1.x, d4), v5 = val(c1.y, w1.y, d5), v6 = val(c1.z, w1.z, d6), v7 = val(c1.w, w1.w, d7);
-  const int64_t o = static_cast<int64_t>(row) * p.n + col;
+  const uint64_t o = static_cast<uint64_t>(static_cast<uint32_t>(row)) * static_cast<uint32_t>(p.n) + static_cast<uint32_t>(col);
   if (p.out_bf16) {
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + o) =
         make_uint4(pack_bf16x2(v0, v1), pack_bf16x2(v2, v3), pack_bf16x2(v4, v5), pack_bf16x2(v6, v7));
@@ -521,16 +521,16 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(Args p) 
 
 // ---------------------------------------------------------------------------
 // out, longer batches: a CTA walks its share of the groups, in order, at its 256
-// columns, with the next group's s and the next two groups' sums in flight while
+// columns, with the next group's s and the next three groups' sums in flight while
 // the current one is multiplied and stored, so that it reads and writes without a
 // pause.  (A warp copies the sums it will use itself, asynchronously, eight lanes a
 // row so that each fetches whole sectors: no registers, no barrier of the CTA.)  Consecutive groups mostly
 // share their adapter, whose rows stay where they are until it changes: in
 // registers up to 32 ranks, in a thread's own places in shared memory beyond.
 // ---------------------------------------------------------------------------
-constexpr int kSumTiles = 3;                // groups' sums in shared memory
+constexpr int kSumTiles = 4;                // groups' sums in shared memory
 constexpr int kSumBytes = kTile * 256 * 4;  // of one group
-constexpr int kRecords = 8, kRecordsAhead = 5;
+constexpr int kRecords = 8, kRecordsAhead = 7;
 
 template <int RK>
 constexpr size_t long_smem() {
@@ -562,13 +562,14 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Arg
   int total = 0;
   for (int c = 0; c < chunks; ++c) total += __ldg(p.counts + c);
   int walk = static_cast<int>(static_cast<int64_t>(total) * blockIdx.x / gridDim.x);
-  const int end = static_cast<int>(static_cast<int64_t>(total) * (blockIdx.x + 1) / gridDim.x), mine = end - walk;
+  const int end = static_cast<int>(static_cast<int64_t>(total) * (blockIdx.x + 1) / gridDim.x);
+  const unsigned mine = end - walk;
   if (mine == 0) {
     griddep_wait();
     return;
   }
   int chunk = 0, base = 0, count = __ldg(p.counts);
-  auto record = [&](int i) {  // requests the record of this CTA's group i (they are asked for in order)
+  auto record = [&](unsigned i) {  // requests the record of this CTA's group i (they are asked for in order)
     if (walk >= end) return;
     while (walk - base >= count) {
       base += count;
@@ -578,21 +579,26 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Arg
     if (tid < kRecord / 4) cp_async16(smem_addr(&recs[i % kRecords][tid * 4]), src + tid * 4, true);
     ++walk;
   };
-  auto sums = [&](int i) {  // requests the sums of group i
-    const int* rec = recs[i % kRecords];
-    const int r0 = lane >> 3, piece = lane & 7, cc = col0 + piece * 4;
-    const uint32_t dst = smem_addr(cs) + (i % kSumTiles) * kSumBytes + warp * (kTile * 128) + r0 * 128 +
-                         (piece ^ (r0 & 1)) * 16;
+  // (a row of c or out is less than 2^26 bytes: an address is one multiply-add)
+  const int r0 = lane >> 3, piece = lane & 7;
+  const bool piece_in = col0 + piece * 4 < p.n;
+  const char* c_col = reinterpret_cast<const char*>(p.c + (piece_in ? col0 + piece * 4 : 0));
+  const uint32_t c_row = static_cast<uint32_t>(p.n) * 4u;
+  const uint32_t cs_put = smem_addr(cs) + warp * (kTile * 128) + r0 * 128 + (piece ^ (r0 & 1)) * 16;
+  auto sums = [&](unsigned i) {  // requests the sums of group i
+    if (i >= mine) return;
+    const int* rec = recs[i % kRecords] + 1 + r0;
+    const uint32_t dst = cs_put + (i % kSumTiles) * kSumBytes;
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
-      const int tok = i < mine ? rec[1 + r0 + h * 4] : -1;
-      const bool on = cc < p.n && tok >= 0;
-      cp_async16(dst + h * 512, p.c + (on ? static_cast<int64_t>(tok) * p.n + cc : 0), on);
+      const int tok = rec[h * 4];
+      cp_async16(dst + h * 512, c_col + static_cast<uint64_t>(static_cast<uint32_t>(max(tok, 0))) * c_row,
+                 piece_in && tok >= 0);
     }
   };
   float sa_n[2];
   float2 s_n[SV];
-  auto fetch = [&](int i) {  // s and the tokens' scales of group i
+  auto fetch = [&](unsigned i) {  // s and the tokens' scales of group i
     if (i >= mine) return;
     const int* rec = recs[i % kRecords];
     const bool has = rec[0] >= 0;
@@ -619,20 +625,20 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Arg
       }
     }
   };
-  for (int i = 0; i < kRecordsAhead; ++i) record(i);
+  for (unsigned i = 0; i < kRecordsAhead; ++i) record(i);
   cp_async_commit();
   cp_async_wait_all();
   __syncthreads();
   fetch(0);
   griddep_wait();
   griddep_launch_dependents();
-  for (int i = 0; i < kSumTiles - 1; ++i) {
+  for (unsigned i = 0; i < kSumTiles - 1; ++i) {
     sums(i);
     cp_async_commit();
   }
   uint32_t bv[4][VEC / 2];
   int held = -1;  // the adapter whose rows are held
-  for (int i = 0; i < mine; ++i) {
+  for (unsigned i = 0; i < mine; ++i) {
     const int* rec = recs[i % kRecords];
     const int use = rec[0], par = i & 1;
     const float sa[2] = {sa_n[0], sa_n[1]};
@@ -658,7 +664,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Arg
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) d[j][e] = 0.0f;
+      for (int e = 0; e < 4; ++e) d[j][e] = use >= 0 ? 0.0f : -0.0f;  // (x + -0 is x, for -0 too)
     if (use >= 0) {
       uint8_t* bs = cs + kSumTiles * kSumBytes + tid * 16;
       if (held != use) {
@@ -734,7 +740,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Arg
       const int tok = rec[1 + g + h * 8];
       if (tok >= 0 && in)
         store8(p, tok, col, *reinterpret_cast<const int4*>(c + h * 1024 + e0),
-               *reinterpret_cast<const int4*>(c + h * 1024 + e1), sa[h], sw[0], sw[1], use >= 0,
+               *reinterpret_cast<const int4*>(c + h * 1024 + e1), sa[h], sw[0], sw[1], true,
                d[0][2 * h], d[0][2 * h + 1], d[1][2 * h], d[1][2 * h + 1], d[2][2 * h], d[2][2 * h + 1], d[3][2 * h],
                d[3][2 * h + 1]);
     }
