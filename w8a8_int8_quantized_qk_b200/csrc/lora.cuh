@@ -7,7 +7,7 @@
 // tokens the sums are the stream of stream.cuh, which runs first and leaves room
 // on its SMs: s is formed beside it (and waits for it at its end, so that the
 // last kernel, which waits for s, waits for both).  Beyond, the GEMM fills the
-// SMs, and s comes first.
+// SMs, and s comes first, after a kernel that groups the tokens.
 //
 // Both small products run on the bf16 matrix instruction, 16 rows at a time.
 // A bf16 value is exact there; a binary32 one (s, and x when it is fp32) enters
@@ -18,7 +18,15 @@
 // beyond (a first kernel sorts those).  So an adapter is read for its own tokens
 // only, however requests are mixed, and one that holds NaN or infinity reaches no
 // other's rows.  (Tiles of 16 tokens in a row, an adapter present there after
-// another, took 299 us for 1024 x 4096 x 4096, rank 128, 24 adapters in any order.)
+// another, took 299 us for 1024 x 4096 x 4096, rank 128, 24 adapters in any order;
+// groups take 87 us.)
+//
+// Bounds.  A few tokens: reading the weights, 4 x 14336 x 4096 rank 16 in 18 us (61
+// MB); 64 x 4096 x 4096 with 32 adapters of rank 64 in 22.7 us (52 MB: the second
+// half of the adapters is read only after the sums).  A prompt: 4096 x 4096 x 4096
+// rank 16 in 103-112 us, of which the GEMM with int32 sums takes 63 (48 with bf16
+// output), s 13, the groups 3.5 and the output 29, which reads the 64 MB of sums
+// and is bound by issuing its instructions (0.5 a cycle of each scheduler).
 #pragma once
 
 #include "qk_common.cuh"

@@ -8,8 +8,8 @@
 // every SM: the loads need no registers and no thread waits for them.  The
 // warp matrix instruction (mma.m16n8k32, fed from registers) was built first;
 // it takes 32 cycles a warp for 512 weight bytes on this part, which is 47 %
-// of the pipe at full HBM rate for 8 tokens and the bound beyond 16, and its
-// chains of dependent products kept 8 tokens of 2 experts at 4.9 TB/s.
+// of the pipe at full HBM rate for 8 tokens and the bound beyond 16: 32 tokens,
+// two each of 8 experts of 4096 x 14336, took 310 us with it, 236 us here.
 //
 // Every CTA takes the same number of 128 x 128-byte blocks, in the order of
 // the tiles (128 rows by all of K), so no SM idles in a last round: a tile that
