@@ -453,6 +453,10 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool v
                "l"(reinterpret_cast<uint64_t>(src)), "r"(valid ? 16 : 0)
                : "memory");
 }
+// the 128-byte line that holds *p, into L2
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
