@@ -165,6 +165,35 @@ def test_one_workspace_for_calls_of_all_kinds():
         assert same(got, want)
 
 
+def test_one_workspace_for_long_batches():
+    """Batches of different lengths, orders of adapters and numbers of groups, one behind another: each writes its
+    groups and sums where the last one's kernels have just read theirs."""
+    need_gpu()
+    g = torch.Generator(device="cuda").manual_seed(9)
+    n, k, rank, adapters = 1032, 528, 24, 7
+    b = torch.randint(-127, 128, (n, k), generator=g, device="cuda", dtype=torch.int8)
+    sw = torch.rand(n, generator=g, device="cuda") / 1000
+    la = (torch.randn((adapters, rank, k), generator=g, device="cuda") / 20).bfloat16()
+    lb = torch.randn((adapters, n, rank), generator=g, device="cuda").bfloat16()
+    ws = torch.full((32 << 20,), 255, dtype=torch.uint8, device="cuda")
+    calls = []
+    for m in (70, 1024, 2500, 65, 1300):
+        x = torch.randn((m, k), generator=g, device="cuda").bfloat16()
+        a, sa = qk.quantize_per_token(x)
+        ids = torch.randint(-1, adapters, (m,), generator=g, device="cuda", dtype=torch.int32)
+        for order in (ids, torch.sort(ids, descending=True).values, torch.full_like(ids, -1), torch.full_like(ids, 3)):
+            calls.append(lambda ws, a=a, sa=sa, x=x, order=order: qk.w8a8_lora_gemm(
+                a, b, sa, sw, x, la, lb, order, workspace=ws))
+    want = []
+    for call in calls:
+        want.append(call(None))
+        torch.cuda.synchronize()
+    for _ in range(5):
+        got = [call(ws) for call in calls]
+        got += [call(ws) for call in reversed(calls)]
+        assert same(got, want + want[::-1])
+
+
 def test_projection_captured_with_split_k():
     """The GEMM's own workspace has to be cleared in the replay too."""
     need_gpu()
