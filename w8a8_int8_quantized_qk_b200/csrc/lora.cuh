@@ -19,7 +19,7 @@
 // only, however requests are mixed, and one that holds NaN or infinity reaches no
 // other's rows.  (Tiles of 16 tokens in a row, an adapter present there after
 // another, took 299 us for 1024 x 4096 x 4096, rank 128, 24 adapters in any order;
-// groups take 87 us.)
+// groups take 77 us.)
 //
 // Bounds.  A few tokens: reading the weights, 4 x 14336 x 4096 rank 16 in 18 us (61
 // MB); 64 x 4096 x 4096 with 32 adapters of rank 64 in 22.1 us (52 MB: the output
@@ -545,31 +545,39 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(Args p) 
 
 // ---------------------------------------------------------------------------
 // out, longer batches: a CTA walks its share of the groups, in order, at its 256
-// columns, with the next group's s and the next three groups' sums in flight while
-// the current one is multiplied and stored, so that it reads and writes without a
-// pause.  (A warp copies the sums it will use itself, asynchronously, eight lanes a
-// row so that each fetches whole sectors: no registers, no barrier of the CTA.)  Consecutive groups mostly
-// share their adapter, whose rows stay where they are until it changes: in
-// registers up to 32 ranks, in a thread's own places in shared memory beyond.
+// columns, with the next group's s and the next groups' sums in flight while the
+// current one is multiplied and stored, so that it reads and writes without a pause.
+// (A warp copies the sums it will use itself, asynchronously, eight lanes a row so
+// that each fetches whole sectors: no registers, no barrier of the CTA.)  Consecutive
+// groups mostly share their adapter, whose rows stay where they are until it changes:
+// in registers up to 32 ranks, in a thread's own places in shared memory beyond.
 // ---------------------------------------------------------------------------
-constexpr int kSumTiles = 4;                // groups' sums in shared memory
 constexpr int kSumBytes = kTile * 256 * 4;  // of one group
 constexpr int kRecords = 8, kRecordsAhead = 7;
 
+// Groups' sums in shared memory, and buffers of s: two CTAs an SM at 128 ranks too
+// (4096 x 2048 x 2048, 24 mixed adapters: 106 us with one CTA and four groups, 97 us
+// so).
+template <int RK>
+constexpr int kSumTiles = RK > 64 ? 2 : 4;
+template <int RK>
+constexpr int kTermBuffers = RK > 64 ? 1 : 2;
+
 template <int RK>
 constexpr size_t long_smem() {
-  return static_cast<size_t>(kSumTiles) * kSumBytes + (RK > 32 ? kExpandThreads * RK * 2 : 0);
+  return static_cast<size_t>(kSumTiles<RK>) * kSumBytes + (RK > 32 ? kExpandThreads * RK * 2 : 0);
 }
 
 template <int RK>  // ranks, rounded up to 16, 32, 64 or 128
 __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Args p) {
   // ranks a thread takes of a step (as two instructions' operands, or one's)
   constexpr int STEP = RK < 32 ? 16 : 32, STEPS = RK / STEP, HALVES = STEP / 16, VEC = STEP / 4;
+  constexpr int TILES = kSumTiles<RK>, BUFS = kTermBuffers<RK>;
   constexpr int WORDS = RK / 2, PITCH = WORDS + 4, SV = (kTile * WORDS + kExpandThreads - 1) / kExpandThreads;
   // the sums: [group][warp][row][8 pieces of 16 bytes, a pair exchanged in odd rows];
   // the adapter's rows: [step][product][thread][16 bytes]
   extern __shared__ __align__(16) uint8_t cs[];
-  __shared__ __align__(16) uint32_t ss[2][3][kTile][PITCH];  // s: [buffer][term][row][pair of ranks]
+  __shared__ __align__(16) uint32_t ss[BUFS][3][kTile][PITCH];  // s: [buffer][term][row][pair of ranks]
   __shared__ __align__(16) int recs[kRecords][kRecord];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
   const int col0 = blockIdx.y * 256 + warp * 32, col = col0 + q * 8;
@@ -612,7 +620,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Arg
   auto sums = [&](unsigned i) {  // requests the sums of group i
     if (i >= mine) return;
     const int* rec = recs[i % kRecords] + 1 + r0;
-    const uint32_t dst = cs_put + (i % kSumTiles) * kSumBytes;
+    const uint32_t dst = cs_put + (i % TILES) * kSumBytes;
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
       const int tok = rec[h * 4];
@@ -656,7 +664,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Arg
   fetch(0);
   griddep_wait();
   griddep_launch_dependents();
-  for (unsigned i = 0; i < kSumTiles - 1; ++i) {
+  for (unsigned i = 0; i < TILES - 1; ++i) {
     sums(i);
     cp_async_commit();
   }
@@ -664,8 +672,9 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Arg
   int held = -1;  // the adapter whose rows are held
   for (unsigned i = 0; i < mine; ++i) {
     const int* rec = recs[i % kRecords];
-    const int use = rec[0], par = i & 1;
+    const int use = rec[0], par = i % BUFS;
     const float sa[2] = {sa_n[0], sa_n[1]};
+    if (BUFS == 1 && i > 0) __syncthreads();  // (s of the last group has been read)
     if (use >= 0) {
 #pragma unroll
       for (int v = 0; v < SV; ++v) {
@@ -680,7 +689,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Arg
     }
     // (s and the records that were waited for below are there for every thread)
     __syncthreads();
-    sums(i + kSumTiles - 1);
+    sums(i + TILES - 1);
     record(i + kRecordsAhead);
     cp_async_commit();
     fetch(i + 1);
@@ -690,11 +699,12 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Arg
 #pragma unroll
       for (int e = 0; e < 4; ++e) d[j][e] = use >= 0 ? 0.0f : -0.0f;  // (x + -0 is x, for -0 too)
     if (use >= 0) {
-      uint8_t* bs = cs + kSumTiles * kSumBytes + tid * 16;
+      uint8_t* bs = cs + TILES * kSumBytes + tid * 16;
       if (held != use) {
         const __nv_bfloat16* b = p.lb + static_cast<int64_t>(use) * p.n * p.rank;
 #pragma unroll
-        for (int st = 0; st < STEPS; ++st)
+        for (int st = 0; st < STEPS; ++st) {
+          if (RK > 64 && st * STEP >= p.rank) break;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int r = st * STEP + q * VEC, cb = col0 + (g >> 1) * 8 + j * 2 + (g & 1);
@@ -714,6 +724,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Arg
               bv[j][1] = v.y;
             }
           }
+        }
         if constexpr (RK > 32) {
           cp_async_commit();
           cp_async_wait_all();
@@ -722,6 +733,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Arg
       }
 #pragma unroll
       for (int st = 0; st < STEPS; ++st) {
+        if (RK > 64 && st * STEP >= p.rank) break;
         if constexpr (RK > 32) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -755,9 +767,9 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Arg
         }
       }
     }
-    cp_async_wait_but<kSumTiles - 1>();
+    cp_async_wait_but<TILES - 1>();
     __syncwarp();  // (the warp's lanes copied them for one another)
-    const uint8_t* c = cs + (i % kSumTiles) * kSumBytes + warp * (kTile * 128) + g * 128;
+    const uint8_t* c = cs + (i % TILES) * kSumBytes + warp * (kTile * 128) + g * 128;
     const int e0 = ((2 * q) ^ (g & 1)) * 16, e1 = ((2 * q + 1) ^ (g & 1)) * 16;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -883,10 +895,9 @@ inline cudaError_t launch_expand(const Args& a, int dev, int num_sms, cudaStream
     const dim3 grid(most_groups(a.m, a.adapters, true), (a.n + kExpandCols - 1) / kExpandCols);
     return launch_pdl(lora_expand_kernel, grid, dim3(kExpandThreads), expand_smem(a.rank), stream, 1, a);
   }
-  // as many CTAs as are resident at once (two an SM, one at 128 ranks), at least one
-  // a column block
+  // as many CTAs as are resident at once (two an SM), at least one a column block
   const int most = chunks_of(a.m) * a.most, cols = (a.n + 255) / 256;
-  int x = (a.rank <= 64 ? 2 : 1) * num_sms / cols;
+  int x = 2 * num_sms / cols;
   x = x < 1 ? 1 : (x > most ? most : x);
   const dim3 grid(x, cols);
   if (a.rank <= 16) return launch_long<16>(a, grid, dev, stream);
