@@ -87,8 +87,8 @@ struct Args {
   void* out;        // [m, n] or null
   int out_bf16;
   int tiles_m, tiles_n, num_kb, groups;
-  // 1 when bf16 `out` (and no `c`) is written by TMA bulk tensor stores
-  // from shared memory (tensor map tmO)
+  // 1 when bf16 `out` (and no `c`), 2 when `c` (and no `out`) is written by TMA
+  // bulk tensor stores from shared memory (tensor map tmO)
   int tma_out;
   // 1: a and b are float8 e4m3 codes, the MMA is kind::f8f6f4 and the
   // accumulator fp32 (channel and pair kernels, whole tiles or the cluster
@@ -384,8 +384,8 @@ __device__ __forceinline__ void store8_channel(const Args& p, int row, int col, 
   }
 }
 
-// bf16 output staging of one epilogue warp: a 32-row x 32-column box
-// (64 bytes a row) for one TMA store
+// Output staging of one epilogue warp: a box of 32 rows x 64 bytes (32 bf16
+// outputs or 16 int32 sums a row) for one TMA store
 constexpr int kOutBoxBytes = 32 * 32 * 2;
 
 // The accumulator's value as binary32: an int32 sum converted (exact below
@@ -474,6 +474,25 @@ __device__ __forceinline__ void store32_channel(const Args& p, int row, int col0
   }
 }
 
+// Writes the warp's 16 words a row into its staging box and stores that at (col,
+// row0), after the previous copy has read it.
+__device__ __forceinline__ void store_box(const CUtensorMap* tmO, uint8_t* box, int col, int row0, int lane,
+                                          const uint32_t* w) {
+  if (lane == 0) bulk_wait_read_all();
+  __syncwarp();
+  const uint32_t rowaddr = smem_addr(box) + static_cast<uint32_t>(lane) * 64u;
+  const uint32_t sx = (static_cast<uint32_t>(lane) >> 1) & 3u;
+#pragma unroll
+  for (uint32_t j = 0; j < 4; ++j)
+    st_shared_v4(rowaddr + ((j ^ sx) << 4), w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(tmO, smem_addr(box), col, row0);
+    bulk_commit();
+  }
+}
+
 // 32 bf16 outputs of one row (columns col0 .. col0 + 31), converted exactly
 // as store32_channel does, written by the warp into its staging box (row r =
 // lane at byte 64 r; 64-byte swizzle: 16-byte chunk j of row r sits at
@@ -486,12 +505,23 @@ __device__ __forceinline__ void store32_channel(const Args& p, int row, int col0
 // form): half the FMA-pipe instructions, which compete with the tensor
 // core's MMAs on the same SM (0.6 us of a 52 us prefill GEMM).  (Leaving
 // out the exact multiply by an output_scale of 1 measured no faster.)
+// With tma_out 2 the sums themselves are written, in two boxes of 16 columns:
+// 16-byte stores from registers fill half a 32-byte sector each (4096 x 4096 x 4096:
+// 63 us with those, 55 us so).
 template <bool F8 = false>
 __device__ __forceinline__ void store32_tma(const Args& p, const CUtensorMap* tmO, uint8_t* box,
                                             int row0, int col0, float sa, const float* sw,
                                             const uint32_t (&v)[32]) {
   if (col0 >= p.n || row0 >= p.m) return;  // the box lies wholly outside (warp-uniform)
   const int lane = threadIdx.x & 31;
+  if constexpr (!F8) {
+    if (p.tma_out == 2) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (col0 + h * 16 < p.n) store_box(tmO, box, col0 + h * 16, row0, lane, v + h * 16);
+      return;
+    }
+  }
   uint32_t w[16];
   const uint64_t sa2 = pack2(__float_as_uint(sa), __float_as_uint(sa));
   const uint64_t al2 = pack2(__float_as_uint(p.alpha), __float_as_uint(p.alpha));
@@ -508,19 +538,7 @@ __device__ __forceinline__ void store32_tma(const Args& p, const CUtensorMap* tm
     t = f32x2_mul(f32x2_mul(f32x2_mul(t, sa2), s2), al2);
     w[j] = pack_bf16x2(lo_of(t), hi_of(t));
   }
-  if (lane == 0) bulk_wait_read_all();
-  __syncwarp();
-  const uint32_t rowaddr = smem_addr(box) + static_cast<uint32_t>(lane) * 64u;
-  const uint32_t sx = (static_cast<uint32_t>(lane) >> 1) & 3u;
-#pragma unroll
-  for (uint32_t j = 0; j < 4; ++j)
-    st_shared_v4(rowaddr + ((j ^ sx) << 4), w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    tma_store_2d(tmO, smem_addr(box), col0, row0);
-    bulk_commit();
-  }
+  store_box(tmO, box, col0, row0, lane, w);
 }
 
 // Per-channel epilogue, 4 warps; warp w owns TMEM lanes 32*(w%4) (rows)

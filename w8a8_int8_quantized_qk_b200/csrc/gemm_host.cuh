@@ -41,17 +41,17 @@ inline bool make_tmap(CUtensorMap* map, const void* base, int rows, int k, int b
          CUDA_SUCCESS;
 }
 
-// bf16 [rows, cols] row-major output, box = 32 columns (64 bytes) x 32 rows,
-// 64-byte swizzle (the layout store32_tma writes); stores are clipped to
-// the tensor.
-inline bool make_out_tmap(CUtensorMap* map, const void* base, int rows, int cols) {
+// bf16 output or int32 sums [rows, cols], row-major: box = 64 bytes (32 or 16
+// columns) x 32 rows, 64-byte swizzle (the layout store32_tma writes); stores are
+// clipped to the tensor.
+inline bool make_out_tmap(CUtensorMap* map, const void* base, int rows, int cols, bool sums) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
-  const cuuint32_t box[2] = {32, 32};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * (sums ? 4 : 2)};
+  const cuuint32_t box[2] = {sums ? 16u : 32u, 32};
   const cuuint32_t estr[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+  return fn(map, sums ? CU_TENSOR_MAP_DATA_TYPE_INT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -59,8 +59,8 @@ inline bool make_out_tmap(CUtensorMap* map, const void* base, int rows, int cols
 // Tensor maps depend only on (base, rows, k, box_rows, kind): the recent
 // ones are kept so that repeated calls on the same buffers skip the
 // driver's encoder (a few microseconds of host time per map).  kind 0: an
-// int8 operand (make_tmap); kind 1: a bf16 output (make_out_tmap, k =
-// columns).
+// int8 operand (make_tmap); kind 1: a bf16 output, 2: int32 sums (make_out_tmap,
+// k = columns).
 inline bool cached_tmap(CUtensorMap* map, const void* base, int rows, int k, int box_rows,
                         int kind = 0) {
   struct Entry {
@@ -80,7 +80,7 @@ inline bool cached_tmap(CUtensorMap* map, const void* base, int rows, int k, int
       return true;
     }
   }
-  if (!(kind == 1 ? make_out_tmap(map, base, rows, k) : make_tmap(map, base, rows, k, box_rows)))
+  if (!(kind ? make_out_tmap(map, base, rows, k, kind == 2) : make_tmap(map, base, rows, k, box_rows)))
     return false;
   Entry& e = entries[next];
   e.base = base;
@@ -292,6 +292,12 @@ inline size_t pair_workspace_bytes(const PairPlan& pl) {
   return kCounterHeaderBytes + static_cast<size_t>(pl.tiles) * 16 * 32 * (kPairBN / 2) * 4;
 }
 
+// What store32_tma writes of a call (Args::tma_out).
+inline int tma_out_of(const Args& a) {
+  if (a.c == nullptr) return a.out != nullptr && a.out_bf16 ? 1 : 0;
+  return a.out == nullptr && !a.f8 ? 2 : 0;
+}
+
 // CTA-pair kernel for m > 128.  0 ok, 1 tensor-map failure, 2 CUDA error.
 inline int launch_pair(Args a, const int8_t* A, const int8_t* B, int dev, int num_sms,
                        void* workspace, cudaStream_t stream, cudaError_t* err,
@@ -328,10 +334,10 @@ inline int launch_pair(Args a, const int8_t* A, const int8_t* B, int dev, int nu
   }
   CUtensorMap ta, tb, to;
   if (!cached_tmap(&ta, A, a.m, a.k, 128) || !cached_tmap(&tb, B, a.n, a.k, 128)) return 1;
-  // bf16 out without c, outside split-K: TMA stores from shared memory
-  a.tma_out = (a.out != nullptr && a.out_bf16 && a.c == nullptr && a.sk.splits == 1) ? 1 : 0;
+  // one of bf16 out and c, outside split-K: TMA stores from shared memory
+  a.tma_out = a.sk.splits == 1 ? tma_out_of(a) : 0;
   if (a.tma_out) {
-    if (!cached_tmap(&to, a.out, a.m, a.n, 32, 1)) return 1;
+    if (!cached_tmap(&to, a.tma_out == 2 ? a.c : a.out, a.m, a.n, 32, a.tma_out)) return 1;
   } else {
     to = ta;  // unused
   }
@@ -633,10 +639,10 @@ inline int launch(Args a, const int8_t* A, const int8_t* B, bool group, int dev,
   }
   CUtensorMap ta, tb, to;
   if (!cached_tmap(&ta, A, a.m, a.k, BM) || !cached_tmap(&tb, B, a.n, a.k, bn)) return 1;
-  // channel kernel, bf16 out without c: TMA stores from shared memory
-  a.tma_out = (!group && a.out != nullptr && a.out_bf16 && a.c == nullptr) ? 1 : 0;
+  // channel kernel, one of bf16 out and c: TMA stores from shared memory
+  a.tma_out = group ? 0 : tma_out_of(a);
   if (a.tma_out) {
-    if (!cached_tmap(&to, a.out, a.m, a.n, 32, 1)) return 1;
+    if (!cached_tmap(&to, a.tma_out == 2 ? a.c : a.out, a.m, a.n, 32, a.tma_out)) return 1;
   } else {
     to = ta;  // unused
   }
