@@ -30,9 +30,9 @@
  *   allows it early (this library's kernels do; a kernel that does not is
  *   waited for in full).  Each kernel waits for its predecessor before it
  *   reads anything the predecessor may write or writes anything it may read,
- *   with one exception: the GEMMs (qk_w8a8_gemm and its variants) and the
- *   linear layer request their first weight tiles b (never scale_b or any
- *   other input) before that wait.  So the kernel launched just before a GEMM
+ *   with one exception: the GEMMs (qk_w8a8_gemm and its variants,
+ *   qk_w8a8_lora_gemm among them) and the linear layer request their first
+ *   weight tiles b (never scale_b or any other input) before that wait.  So the kernel launched just before a GEMM
  *   on the same stream must not write that GEMM's b if it triggers its
  *   dependents early; the quantisers of this library never write weights.
  * - Values of int8 operands are in [-127, 127] (what the quantisers
