@@ -453,8 +453,20 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(Args p) 
     const int tok = gr.tok[g + h * 8];
     sa[h] = tok >= 0 ? __ldg(p.sa + tok) : 0.0f;
   }
+  // s of pair of ranks w of a row, its K parts
+  auto s_of = [&](int i, float2 (&f)[kMaxParts]) {
+    const int row = i / (steps * 16), w = i - row * (steps * 16), tok = gr.tok[row];
+    const bool on = tok >= 0 && 2 * w < p.rank;
+    const float* s = p.s + static_cast<int64_t>(on ? tok : 0) * p.rank + (on ? 2 * w : 0);
+#pragma unroll
+    for (int z = 0; z < kMaxParts; ++z)
+      f[z] = on && z < p.kparts ? *reinterpret_cast<const float2*>(s + static_cast<int64_t>(z) * p.m * p.rank)
+                                : make_float2(0.0f, 0.0f);
+  };
   griddep_wait();
   griddep_launch_dependents();
+  float2 f[kMaxParts];  // (requested before the sums: its use comes first)
+  if (use >= 0) s_of(tid, f);
   int4 c0[kHalves][2], c1[kHalves][2];  // the sums of rows g and g + 8
 #pragma unroll
   for (int v = 0; v < kHalves; ++v) {
@@ -487,22 +499,15 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(Args p) 
   }
   if (use >= 0) {
     for (int i = tid; i < kTile * steps * 16; i += kExpandThreads) {
-      const int row = i / (steps * 16), w = i - row * (steps * 16), r = 2 * w, tok = gr.tok[row];
-      uint32_t term[3] = {0, 0, 0};
-      if (tok >= 0 && r < p.rank) {
-        const float* s = p.s + static_cast<int64_t>(tok) * p.rank + r;
-        float2 f[kMaxParts];
+      const int row = i / (steps * 16), w = i - row * (steps * 16);
+      if (i != tid) s_of(i, f);
 #pragma unroll
-        for (int z = 0; z < kMaxParts; ++z)
-          f[z] = z < p.kparts ? *reinterpret_cast<const float2*>(s + static_cast<int64_t>(z) * p.m * p.rank)
-                              : make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int z = 1; z < kMaxParts; ++z) {
-          f[0].x += f[z].x;
-          f[0].y += f[z].y;
-        }
-        split3(f[0].x, f[0].y, term);
+      for (int z = 1; z < kMaxParts; ++z) {
+        f[0].x += f[z].x;
+        f[0].y += f[z].y;
       }
+      uint32_t term[3];
+      split3(f[0].x, f[0].y, term);
 #pragma unroll
       for (int e = 0; e < 3; ++e) ss[(e * kTile + row) * pitch + w] = term[e];
     }
