@@ -111,18 +111,24 @@ __device__ __forceinline__ bool gather_unit(const Args& p, int u, bool none, Gro
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     id[h] = h * 32 + lane < p.m ? adapter_of(p, h * 32 + lane) : -2;
-    same[h] = static_cast<uint64_t>(__match_any_sync(0xFFFFFFFFu, id[h])) << (32 * h);
+    same[h] = 0;
   }
+  const int halves = p.m > 32 ? 2 : 1;
+  same[0] = __match_any_sync(0xFFFFFFFFu, id[0]);
+  if (halves == 2) {
+    same[1] = static_cast<uint64_t>(__match_any_sync(0xFFFFFFFFu, id[1])) << 32;
 #pragma unroll 8
-  for (int j = 0; j < 32; ++j) {
-    const int lo = __shfl_sync(0xFFFFFFFFu, id[0], j), hi = __shfl_sync(0xFFFFFFFFu, id[1], j);
-    if (id[1] == lo) same[1] |= 1ull << j;
-    if (id[0] == hi) same[0] |= 1ull << (32 + j);
+    for (int j = 0; j < 32; ++j) {
+      const int lo = __shfl_sync(0xFFFFFFFFu, id[0], j), hi = __shfl_sync(0xFFFFFFFFu, id[1], j);
+      if (id[1] == lo) same[1] |= 1ull << j;
+      if (id[0] == hi) same[0] |= 1ull << (32 + j);
+    }
   }
   int base = 0;
   bool found = false;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
+    if (h == halves) break;
     const bool leads = id[h] >= (none ? -1 : 0) && (same[h] & ((1ull << (32 * h + lane)) - 1ull)) == 0;
     const int units = leads ? (__popcll(same[h]) + kTile - 1) / kTile : 0;
     int sum = units;  // inclusive prefix
@@ -811,12 +817,16 @@ struct Dense {
 
 __global__ void __launch_bounds__(stream::kThreads, 1)
     lora_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, int m,
-                       const __grid_constant__ stream::Plan pl, int32_t* c) {
+                       const __grid_constant__ stream::Plan pl, int32_t* c, const int32_t* ids) {
   extern __shared__ uint8_t raw[];
   __shared__ stream::Bars s;
   if (threadIdx.x == 0) {
     prefetch_tmap(&tmW);
     prefetch_tmap(&tmX);
+    if (blockIdx.x == 0) {  // (the next kernel's first read)
+      prefetch_l2(ids);
+      prefetch_l2(ids + m - 1);
+    }
   }
   stream::setup(s, pl);
   stream::run(Dense{m, pl, c}, pl, s, stream::ring_of(raw), &tmW, &tmX);
@@ -883,7 +893,7 @@ inline int launch_stream(const Args& a, const int8_t* x, const int8_t* w, const 
   if ((*err = gemm::set_smem_once(lora_stream_kernel, dev, 0, stream::kRingBytes + 1024)) != cudaSuccess) return 2;
   if ((*err = stream::shares_sm_once(lora_stream_kernel, dev, 0)) != cudaSuccess) return 2;
   *err = launch_pdl(lora_stream_kernel, dim3(num_sms), dim3(stream::kThreads), stream::smem_bytes(pl), stream, 1, tw, tx,
-                    a.m, pl, const_cast<int32_t*>(a.c));
+                    a.m, pl, const_cast<int32_t*>(a.c), a.ids);
   return *err == cudaSuccess ? 0 : 2;
 }
 
