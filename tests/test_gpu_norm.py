@@ -5,8 +5,9 @@ Against the definition, in numpy:
   no sum): t = r * w, a = max |t|, inv = qmax * (1 / a), each step one binary32
   operation;
 * everything against the formula in 64 bits.  With u = 2^-24 (half a binary32 step):
-  - the squares are added by 256 or more threads, so a sum of k of them passes at most k/256 + 16
-    additions: relative error of the sum (k/256 + 16) u, halved by the square root, then the mean, eps,
+  - a square passes at most k/256 + 16 additions: those of its 16-byte vector (8 or 4), of its thread's
+    vectors (1 up to k = 256, 2 to 512, 4 to 1024, never more than 8), 5 in the warp, 5 between warps (none up
+    to k = 1024): relative error of the sum (k/256 + 16) u, halved by the square root, then the mean, eps,
     square root and reciprocal: rstd within ((k/256 + 16)/2 + 4) u;
   - scale: + 3 u (a's own rounding, z, the division); norm_out in binary32: + 2 u (t, the product);
     in bf16 half a step, 2^-8, more;
@@ -100,6 +101,17 @@ SHAPES = [(1, 16), (1, 4096), (2, 48), (3, 64), (5, 528), (64, 8192), (147, 1040
 def test_norm_int8(O, m, k, bf16):
     x, res, w = make(m, k, bf16, seed=m + k)
     got = qk.add_rmsnorm_quant_per_token(x_dev(x), x_dev(w), x_dev(res), 1e-6, want_norm=True)
+    check(O, x, res, w, 1e-6, got)
+
+
+@pytest.mark.parametrize("vectors", [2, 32, 34, 64, 66, 128, 130, 256, 258, 512, 514])
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("residual", [True, False])
+def test_norm_many_rows_of_every_width(O, vectors, bf16, residual):
+    """Both sides of every choice of threads and vectors a thread, for rows enough to be walked."""
+    m, k = 700, vectors * (8 if bf16 else 4) // 16 * 16 or 16
+    x, res, w = make(m, k, bf16, seed=vectors, residual=residual)
+    got = qk.add_rmsnorm_quant_per_token(x_dev(x), x_dev(w), x_dev(res) if residual else None, 1e-6, want_norm=True)
     check(O, x, res, w, 1e-6, got)
 
 

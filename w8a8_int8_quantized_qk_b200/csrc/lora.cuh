@@ -21,8 +21,8 @@
 // another, took 299 us for 1024 x 4096 x 4096, rank 128, 24 adapters in any order;
 // groups take 73 us.)
 //
-// Bounds.  A few tokens: reading the weights, 4 x 14336 x 4096 rank 16 in 18 us (61
-// MB); 64 x 4096 x 4096 with 32 adapters of rank 64 in 22.1 us (52 MB: the output
+// Bounds.  A few tokens: reading the weights, 4 x 14336 x 4096 rank 16 in 17 us (61
+// MB); 64 x 4096 x 4096 with 32 adapters of rank 64 in 21.9 us (52 MB: the output
 // kernel takes its half of the adapters from L2, but only after the sums).  A
 // prompt: 4096 x 4096 x 4096 rank 16 in 93 us, of which the GEMM with int32 sums
 // takes 55 (48 with bf16 output), s 13, the groups 3.5 and the output 29, which reads

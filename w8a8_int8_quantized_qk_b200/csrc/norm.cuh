@@ -21,7 +21,8 @@
 // (as 16-byte vectors of the stream's type, which r is exact in), many rows are
 // walked by persistent CTAs that load a row ahead, and a row is split over a
 // cluster when rows are few.  4096 x 4096 bf16 with residual (117 MB): 29.2 us with
-// the row read twice, 16.2 us here (its own last writes stay in L2).
+// the row read twice, 20.7 us here (5.7 TB/s, 0.87 of the copy rate), 16.2 us into
+// outputs that are still in L2.
 #pragma once
 
 #include "qk_common.cuh"
@@ -227,7 +228,10 @@ __global__ void __launch_bounds__(quant::kMaxThreads) norm_quant_rows_kernel(Arg
 
 // Many rows: persistent CTAs of T threads with V vectors each, the next row's
 // loads in flight.  The warps' sums alternate between two buffers, so a row costs
-// one barrier.  Up to 4 vectors (T = 256) a thread's share of the weight stays in
+// one barrier.  Short rows get few threads with up to 4 vectors each, so that many
+// rows are in flight on an SM and their reductions and barriers stay small (8192 x
+// 512 bf16 with residual: 17.7 us with 256 threads a row, 6.8 with 32; 8192 x 1024:
+// 18.3 and 11.8).  Up to 4 vectors a thread's share of the weight stays in
 // registers; longer rows (T = 512) read it again from cache.
 template <bool BF16, bool RES, int V, int T>
 __global__ void __launch_bounds__(T) norm_quant_persistent_kernel(Args p) {
@@ -269,14 +273,15 @@ __global__ void __launch_bounds__(T) norm_quant_persistent_kernel(Args p) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int v = tid + j * T;
-      float t[E];
+      float t[E], sj = 0.0f;  // (a vector's squares on their own: a short chain)
       if constexpr (RES) {
         xc[j] = add_rows<BF16>(xc[j], dc[j]);
         if (p.res_out != nullptr && v < nvec)
           *reinterpret_cast<uint4*>(static_cast<char*>(p.res_out) + row * p.ldo * ES + static_cast<int64_t>(v) * 16) =
               xc[j];
       }
-      weigh<BF16>(xc[j], KEEP ? w[KEEP ? j : 0] : weight(j), t, a, ss);
+      weigh<BF16>(xc[j], KEEP ? w[KEEP ? j : 0] : weight(j), t, a, sj);
+      ss = __fadd_rn(ss, sj);
     }
     a = quant::warp_max(a);
     ss = warp_sum(ss);
@@ -395,7 +400,8 @@ inline cudaError_t launch_persistent(const Args& a, int num_sms, cudaStream_t st
       cudaGetLastError();
       per = 1;
     }
-    per = per < 8 ? per : 8;
+    constexpr int most = T < 128 ? 1024 / T : 8;
+    per = per < most ? per : most;
     cached.store(per, std::memory_order_relaxed);
   }
   const int cap = per * num_sms, grid = a.m < cap ? a.m : cap;
@@ -404,8 +410,11 @@ inline cudaError_t launch_persistent(const Args& a, int num_sms, cudaStream_t st
 
 template <bool BF16, bool RES>
 inline cudaError_t launch_many(const Args& a, int nvec, int num_sms, cudaStream_t stream) {
-  if (nvec <= 256) return launch_persistent<BF16, RES, 1, 256>(a, num_sms, stream);
-  if (nvec <= 512) return launch_persistent<BF16, RES, 2, 256>(a, num_sms, stream);
+  if (nvec <= 32) return launch_persistent<BF16, RES, 1, 32>(a, num_sms, stream);
+  if (nvec <= 64) return launch_persistent<BF16, RES, 2, 32>(a, num_sms, stream);
+  if (nvec <= 128) return launch_persistent<BF16, RES, 4, 32>(a, num_sms, stream);
+  if (nvec <= 256) return launch_persistent<BF16, RES, 4, 64>(a, num_sms, stream);
+  if (nvec <= 512) return launch_persistent<BF16, RES, 4, 128>(a, num_sms, stream);
   if (nvec <= 1024) return launch_persistent<BF16, RES, 4, 256>(a, num_sms, stream);
   if (nvec <= 5 * 512) return launch_persistent<BF16, RES, 5, 512>(a, num_sms, stream);
   return launch_persistent<BF16, RES, 8, 512>(a, num_sms, stream);
