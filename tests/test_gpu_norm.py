@@ -104,7 +104,7 @@ def test_norm_int8(O, m, k, bf16):
     check(O, x, res, w, 1e-6, got)
 
 
-@pytest.mark.parametrize("vectors", [2, 32, 34, 64, 66, 128, 130, 256, 258, 512, 514])
+@pytest.mark.parametrize("vectors", [2, 32, 34, 64, 66, 128, 130, 256, 258, 512, 514, 1024, 1026, 1536, 1538, 2052])
 @pytest.mark.parametrize("bf16", [True, False])
 @pytest.mark.parametrize("residual", [True, False])
 def test_norm_many_rows_of_every_width(O, vectors, bf16, residual):

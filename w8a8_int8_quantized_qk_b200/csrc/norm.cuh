@@ -231,14 +231,19 @@ __global__ void __launch_bounds__(quant::kMaxThreads) norm_quant_rows_kernel(Arg
 // one barrier.  Short rows get few threads with up to 4 vectors each, so that many
 // rows are in flight on an SM and their reductions and barriers stay small (8192 x
 // 512 bf16 with residual: 17.7 us with 256 threads a row, 6.8 with 32; 8192 x 1024:
-// 18.3 and 11.8).  Up to 4 vectors a thread's share of the weight stays in
-// registers; longer rows (T = 512) read it again from cache.
+// 18.3 and 11.8).  With 256 threads at most a thread's share of the weight stays in
+// registers; longer rows (T = 512) read it again from cache, and skip the last of 3
+// or 5 vectors where they end before it (1500 x 10240: 26.2 us with 5 vectors and no
+// skip, 22.8 with 3; 2049 x 8208 fp32 without residual: 18.5 and 17.8).
 template <bool BF16, bool RES, int V, int T>
 __global__ void __launch_bounds__(T) norm_quant_persistent_kernel(Args p) {
   constexpr int E = BF16 ? 8 : 4;
   constexpr int ES = BF16 ? 2 : 4;
   constexpr int NW = T / 32;
-  constexpr bool KEEP = V <= 4;
+  constexpr bool KEEP = T < 512;
+  // the last vectors are skipped where the row has none there (not with so many
+  // registers in use that the branch costs more: 1000 x 18000 with residual 25.3 us, 26.5)
+  constexpr bool SHORT = !KEEP && (V == 3 || (V == 5 && !RES));
   __shared__ float2 red[2][NW];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nvec = p.k / E;
@@ -273,6 +278,7 @@ __global__ void __launch_bounds__(T) norm_quant_persistent_kernel(Args p) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int v = tid + j * T;
+      if (SHORT && j + 1 == V && v >= nvec) break;
       float t[E], sj = 0.0f;  // (a vector's squares on their own: a short chain)
       if constexpr (RES) {
         xc[j] = add_rows<BF16>(xc[j], dc[j]);
@@ -416,6 +422,7 @@ inline cudaError_t launch_many(const Args& a, int nvec, int num_sms, cudaStream_
   if (nvec <= 256) return launch_persistent<BF16, RES, 4, 64>(a, num_sms, stream);
   if (nvec <= 512) return launch_persistent<BF16, RES, 4, 128>(a, num_sms, stream);
   if (nvec <= 1024) return launch_persistent<BF16, RES, 4, 256>(a, num_sms, stream);
+  if (nvec <= 3 * 512) return launch_persistent<BF16, RES, 3, 512>(a, num_sms, stream);
   if (nvec <= 5 * 512) return launch_persistent<BF16, RES, 5, 512>(a, num_sms, stream);
   return launch_persistent<BF16, RES, 8, 512>(a, num_sms, stream);
 }
