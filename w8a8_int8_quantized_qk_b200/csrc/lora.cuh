@@ -24,7 +24,7 @@
 // Bounds.  A few tokens: reading the weights, 4 x 14336 x 4096 rank 16 in 17 us (61
 // MB); 64 x 4096 x 4096 with 32 adapters of rank 64 in 21.9 us (52 MB: the output
 // kernel takes its half of the adapters from L2, but only after the sums).  A
-// prompt: 4096 x 4096 x 4096 rank 16 in 93 us, of which the GEMM with int32 sums
+// prompt: 4096 x 4096 x 4096 rank 16 in 93-103 us, of which the GEMM with int32 sums
 // takes 55 (48 with bf16 output), s 13, the groups 3.5 and the output 29, which reads
 // the 64 MB of sums: its registers leave four warps a scheduler, each in a
 // chain of shared-memory reads, products and conversions (0.44 instructions a cycle
