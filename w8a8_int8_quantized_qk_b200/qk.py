@@ -325,6 +325,17 @@ def _need_cuda(*ts) -> None:
             raise ValueError("libqk works on CUDA tensors only (no CPU fallback)")
 
 
+def _own_bytes(workspace) -> int:
+    """Bytes a kernel may use from a workspace's address on: those of a dense CUDA tensor.  (An expanded tensor
+    has fewer bytes than elements, and the gaps of a strided view belong to somebody else.)"""
+    if workspace is None:
+        return 0
+    _need_cuda(workspace)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+    return workspace.numel() * workspace.element_size()
+
+
 def quantize_per_token(x, q=None, scale=None, stream=None):
     """x [m, k] bf16/fp32 (CUDA, contiguous) -> (q int8 [m, k], scale fp32 [m])."""
     torch = _torch()
@@ -408,7 +419,7 @@ def w8a8_gemm(a, b, scale_a, scale_b, group_k: int = 0, output_scale: float = 1.
     code = _dtype_code(out) if out is not None else QK_BF16
     _check(qk_w8a8_gemm(m, n, k, _ptr(a), _ptr(b), _ptr(scale_a), _ptr(scale_b), group_k,
                         float(output_scale), _ptr(c), _ptr(out), code, _ptr(workspace),
-                        0 if workspace is None else workspace.numel(), _stream(stream)),
+                        _own_bytes(workspace), _stream(stream)),
            "qk_w8a8_gemm")
     return out, c
 
@@ -496,7 +507,7 @@ def w8a8_gemm_asym(a, zero_point_a, b, wsum_b, scale_a, scale_b, output_scale: f
     code = _dtype_code(out) if out is not None else QK_BF16
     _check(qk_w8a8_gemm_asym(m, n, k, _ptr(a), _ptr(zero_point_a), _ptr(b), _ptr(wsum_b), _ptr(scale_a),
                              _ptr(scale_b), float(output_scale), _ptr(c), _ptr(out), code, _ptr(workspace),
-                             0 if workspace is None else workspace.numel(), _stream(stream)),
+                             _own_bytes(workspace), _stream(stream)),
            "qk_w8a8_gemm_asym")
     return out, c
 
@@ -535,7 +546,7 @@ def w8a8_linear(x, w_q, sw, group_k: int = 0, output_scale: float = 1.0, out_dty
         workspace = torch.zeros((need,), dtype=torch.uint8, device=x.device)
     _check(qk_w8a8_linear(m, n, k, _ptr(x), _dtype_code(x), _ptr(w_q), _ptr(sw), group_k,
                           float(output_scale), _ptr(sa), _ptr(out), _dtype_code(out), _ptr(workspace),
-                          0 if workspace is None else workspace.numel(), _stream(stream)),
+                          _own_bytes(workspace), _stream(stream)),
            "qk_w8a8_linear")
     return out, sa
 
@@ -557,7 +568,7 @@ def w8a8_linear_fused(x, w_q, sw, output_scale: float = 1.0, out_dtype=None, wan
     if workspace is None:
         workspace = torch.zeros((max(need, 1),), dtype=torch.uint8, device=x.device)
     _check(qk_w8a8_linear_fused(m, n, k, _ptr(x), _dtype_code(x), _ptr(w_q), _ptr(sw), float(output_scale),
-                                _ptr(sa), _ptr(out), _dtype_code(out), _ptr(workspace), workspace.numel(),
+                                _ptr(sa), _ptr(out), _dtype_code(out), _ptr(workspace), _own_bytes(workspace),
                                 _stream(stream)),
            "qk_w8a8_linear_fused")
     return out, sa
@@ -703,7 +714,7 @@ def _workspace(workspace, need: int, dev: int, device):
         return workspace.data_ptr(), need, workspace
     if workspace.get_device() != dev:
         _refuse(workspace, dev, workspace.dtype, workspace.shape, "workspace")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    return workspace.data_ptr(), _own_bytes(workspace), workspace
 
 
 def w8a8_lora_gemm(a, b, scale_a, scale_b, x, lora_a, lora_b, adapter_ids, lora_scale=None,
