@@ -393,7 +393,10 @@ QK_API qk_status qk_w8a8_moe_gemm(int num_experts, int total_m, int n, int k, in
  * sums of exact or binary32 products in an order of the library's choice; out
  * is rounded once.  A row without an adapter gets qk_w8a8_gemm's result bit
  * for bit, whatever the adapters hold, and a row never sees another row's
- * adapter.
+ * adapter.  A binary32 x, and s, count with their 24 bits (down to 2^-134 in
+ * magnitude), over the whole range.  An infinite x, lora_scale or s gives what
+ * the formula gives; an infinity in lora_a (with a binary32 x) or in lora_b may
+ * give NaN instead of an infinity, in the rows that use it alone.
  *
  * m, n, k, a, b, scale_a, scale_b, output_scale, out   as qk_w8a8_gemm with
  *                group_k = 0 (out required; m above 2^20 or n above 16776960:

@@ -79,14 +79,18 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two binary32 values as three pairs of bf16 terms.
+// Two binary32 values as three pairs of bf16 terms.  The first saturates: a value above
+// the largest bf16 one leaves a finite rest (24 bits hold), and an infinite one an
+// infinite rest, which is the second term; its own rest, inf - inf, counts as 0, so that
+// the terms add up to the infinity.  (A NaN is in the first two terms already.)
 __device__ __forceinline__ void split3(float lo, float hi, uint32_t (&t)[3]) {
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    t[i] = pack_bf16x2(lo, hi);
-    lo = __fsub_rn(lo, bf16_lo(t[i]));
-    hi = __fsub_rn(hi, bf16_hi(t[i]));
-  }
+  asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(t[0]) : "f"(hi), "f"(lo));
+  lo = __fsub_rn(lo, bf16_lo(t[0]));
+  hi = __fsub_rn(hi, bf16_hi(t[0]));
+  t[1] = pack_bf16x2(lo, hi);
+  lo = __fsub_rn(lo, bf16_lo(t[1]));
+  hi = __fsub_rn(hi, bf16_hi(t[1]));
+  t[2] = pack_bf16x2(lo == lo ? lo : 0.0f, hi == hi ? hi : 0.0f);
 }
 
 // Place of the n-th (from 0) set bit.
