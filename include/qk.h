@@ -447,8 +447,7 @@ QK_API size_t qk_w8a8_lora_gemm_workspace_size(int m, int n, int k, int rank);
  *
  * m              tokens, 0 .. 64 (0: no-op; more: QK_ERR_UNSUPPORTED)
  * hidden, inter  > 0, multiples of 16, <= 133144 (QK_ERR_OVERFLOW_BOUND)
- * num_experts    1 .. 1024;  topk  1 .. 32 (more: QK_ERR_UNSUPPORTED);
- *                num_experts * 2 * inter and num_experts * hidden below 2^31
+ * num_experts    1 .. 1024;  topk  1 .. 32 (more: QK_ERR_UNSUPPORTED)
  * a, scale_a     [m, hidden] int8, 16-B aligned, and [m] fp32
  * topk_ids, topk_weights   [m, topk] int32 and fp32, 4-B aligned
  * w_gate_up      [num_experts, 2 * inter, hidden] int8: an expert's gate rows,

@@ -786,6 +786,15 @@ qk_status qk_w8a8_lora_gemm(int m, int n, int k, const int8_t* a, const int8_t* 
 namespace {
 constexpr int kMoeLayerTokens = 64, kMoeLayerTopk = 32, kMoeLayerExperts = moe::kMaxExperts;
 
+// A stream counts its blocks in 32 bits (stream::Range, slices_of): all experts' gate and
+// up rows, 2081 row blocks of 1041 K blocks each, are 2.2e9.  The down product has at most
+// one token tile more for each expert and one for every 16 pairs, of 1041 row blocks.
+constexpr int64_t row_blocks(int64_t rows) { return (rows + stream::kRows - 1) / stream::kRows; }
+constexpr int64_t kMostKBlocks = (kMaxK + stream::kK - 1) / stream::kK;
+static_assert(kMoeLayerExperts * row_blocks(2LL * kMaxK) * kMostKBlocks < (1LL << 32) - kMostKBlocks);
+static_assert((kMoeLayerExperts + moe::kMaxPairs / 16) * row_blocks(kMaxK) * kMostKBlocks <
+              (1LL << 32) - kMostKBlocks);
+
 struct MoeLayout {
   size_t gu, part, sh, q, total;  // byte offsets (the pairs' records are at 0)
 };
@@ -819,12 +828,6 @@ qk_status moe_layer_check(int m, int hidden, int inter, int num_experts, int top
       num_experts < 1)
     return QK_ERR_INVALID_ARG;
   if (hidden > kMaxK || inter > kMaxK) return QK_ERR_OVERFLOW_BOUND;
-  if (static_cast<int64_t>(num_experts) * 2 * inter > INT32_MAX ||
-      static_cast<int64_t>(num_experts) * hidden > INT32_MAX)
-    return QK_ERR_INVALID_ARG;
-  // (so that a product has at most 2^31 / 128 tiles and one more for each expert
-  // and each pair, of at most 1041 K blocks: under 2^32 blocks with the pairs'
-  // 2048 and the experts' 1024 row-block remainders)
   if (m > kMoeLayerTokens || topk > kMoeLayerTopk || num_experts > kMoeLayerExperts) return QK_ERR_UNSUPPORTED;
   return QK_OK;
 }
