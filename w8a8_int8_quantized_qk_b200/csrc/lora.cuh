@@ -93,12 +93,6 @@ __device__ __forceinline__ void split3(float lo, float hi, uint32_t (&t)[3]) {
   t[2] = pack_bf16x2(lo == lo ? lo : 0.0f, hi == hi ? hi : 0.0f);
 }
 
-// Place of the n-th (from 0) set bit.
-__device__ __forceinline__ int nth_bit(unsigned mask, int n) {
-  for (; n > 0; --n) mask &= mask - 1u;
-  return __ffs(mask) - 1;
-}
-
 // 16 rows of one adapter (or of none: -1).
 struct Group {
   int use;
@@ -256,7 +250,7 @@ __global__ void __launch_bounds__(kChunk) lora_units_kernel(Args p) {
 // ---------------------------------------------------------------------------
 constexpr int kShrinkThreads = 256;
 constexpr int kShrinkStep = 32;
-constexpr int kMaxRank = 128, kRankGroup = 64;
+constexpr int kRankGroup = 64;
 
 // Elements at .. at + 7 of x, and their four pairs as bf16 terms.
 template <bool BF16>
