@@ -155,9 +155,10 @@ __device__ __forceinline__ bool gather_unit(const Args& p, int u, bool none, Gro
 }
 
 // This CTA's group (blockIdx.x), by all threads; false when there is none.
+template <bool BESIDE>
 __device__ __forceinline__ bool group_of_cta(const Args& p, bool none, Group& gr, int& ok) {
   const int tid = threadIdx.x;
-  if (p.beside) {
+  if constexpr (BESIDE) {
     if (tid < 32) {
       const bool found = gather_unit(p, blockIdx.x, none, gr);
       if (tid == 0) ok = found ? 1 : 0;
@@ -276,7 +277,11 @@ __device__ __forceinline__ void terms_x(const uint4 (&v)[BF16 ? 1 : 2], uint32_t
   }
 }
 
-template <bool BF16, int RT>  // RT: tiles of 8 ranks
+// RT: tiles of 8 ranks.  BESIDE: the sums are formed before s, and beside it; a kernel of
+// its own, since the split of shared memory it asks for to stand beside them stays with a
+// kernel (as one of both, a short batch slowed the long ones after it in the process: 4096
+// x 4096 x 4096 rank 16 from 93 to 101 us, 1024 x 4096 x 4096 rank 128 from 73 to 81).
+template <bool BF16, int RT, bool BESIDE>
 __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_kernel(Args p) {
   constexpr int NW = kShrinkThreads / 32, TERMS = BF16 ? 1 : 3, XV = BF16 ? 1 : 2;
   __shared__ float red[NW][kTile][RT * 8 + 1];
@@ -284,11 +289,11 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_kernel(Args p) 
   __shared__ int ok;
   // (beside the sums: x, the adapters and ids are the caller's, complete before the
   // kernel of the sums let this one start, and s is free)
-  if (!p.beside) griddep_wait();
+  if constexpr (!BESIDE) griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
-  if (!group_of_cta(p, false, gr, ok)) {
-    if (p.beside) griddep_wait();
+  if (!group_of_cta<BESIDE>(p, false, gr, ok)) {
+    if constexpr (BESIDE) griddep_wait();
     return;
   }
   const int use = gr.use, tok0 = gr.tok[g], tok1 = gr.tok[g + 8];
@@ -363,7 +368,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_kernel(Args p) 
     for (int w = 0; w < NW; ++w) v += red[w][row][r];
     s[static_cast<int64_t>(gr.tok[row]) * p.rank + r] = ls * v;
   }
-  if (p.beside) {
+  if constexpr (BESIDE) {
     // The next kernel has no room beside these before the sums are done: its rows of
     // the adapter are brought into L2 meanwhile, a part by each CTA of the group,
     // where that part is no more than its work here (64 x 4096 x 4096 rank 64, 32
@@ -433,7 +438,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(Args p) 
     sw[v][0] = in ? __ldg(reinterpret_cast<const float4*>(p.sw + col)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     sw[v][1] = in ? __ldg(reinterpret_cast<const float4*>(p.sw + col) + 1) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   }
-  if (!group_of_cta(p, true, gr, ok)) {
+  if (!group_of_cta<true>(p, true, gr, ok)) {
     griddep_wait();
     return;
   }
@@ -859,11 +864,10 @@ inline int shrink_parts(int m, int k, int adapters, int num_sms) {
 
 template <bool BF16, int RT>
 inline cudaError_t launch_shrink_rt(const Args& a, dim3 grid, int dev, cudaStream_t stream) {
-  if (a.beside) {
-    const cudaError_t e = stream::shares_sm_once(lora_shrink_kernel<BF16, RT>, dev, (BF16 ? 8 : 0) + RT / 4);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_pdl(lora_shrink_kernel<BF16, RT>, grid, dim3(kShrinkThreads), 0, stream, 1, a);
+  if (!a.beside) return launch_pdl(lora_shrink_kernel<BF16, RT, false>, grid, dim3(kShrinkThreads), 0, stream, 1, a);
+  const cudaError_t e = stream::shares_sm_once(lora_shrink_kernel<BF16, RT, true>, dev, (BF16 ? 8 : 0) + RT / 4);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(lora_shrink_kernel<BF16, RT, true>, grid, dim3(kShrinkThreads), 0, stream, 1, a);
 }
 
 template <bool BF16>
