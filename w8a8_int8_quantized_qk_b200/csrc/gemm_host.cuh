@@ -58,7 +58,9 @@ inline bool make_out_tmap(CUtensorMap* map, const void* base, int rows, int cols
 
 // Tensor maps depend only on (base, rows, k, box_rows, kind): the recent
 // ones are kept so that repeated calls on the same buffers skip the
-// driver's encoder (a few microseconds of host time per map).  kind 0: an
+// driver's encoder.  (A map made anew costs little more than one found: a GEMM
+// call takes 11.5 us of host time on one layer's weights, 11.6 us on 64 layers'
+// in turn; with adapters 15.2 and 15.5.)  kind 0: an
 // int8 operand (make_tmap); kind 1: a bf16 output, 2: int32 sums (make_out_tmap,
 // k = columns).
 inline bool cached_tmap(CUtensorMap* map, const void* base, int rows, int k, int box_rows,

@@ -26,8 +26,8 @@
 // Measured (8 experts of 4096 x 14336): one token with two experts 74 us (352 MB
 // of weights, 4.8 TB/s, 0.73 of the copy rate: the SMs' shares of the bandwidth
 // differ, kernel 1's CTAs end between 29 and 39 us, and kernel 3 cannot read
-// before kernel 2 has the row's scale, about 8 us); 32 tokens 236 us (1.41 GB, 6.0
-// TB/s, 0.92).
+// before kernel 2 has the row's scale, about 8 us); 32 tokens 240 us (1.41 GB, 5.9
+// TB/s, 0.90).
 #pragma once
 
 #include "qk_common.cuh"

@@ -21,7 +21,7 @@
 // (as 16-byte vectors of the stream's type, which r is exact in), many rows are
 // walked by persistent CTAs that load a row ahead, and a row is split over a
 // cluster when rows are few.  4096 x 4096 bf16 with residual (117 MB): 29.2 us with
-// the row read twice, 20.7 us here (5.7 TB/s, 0.87 of the copy rate), 16.2 us into
+// the row read twice, 21.0 us here (5.6 TB/s, 0.86 of the copy rate), 16.0 us into
 // outputs that are still in L2.
 #pragma once
 
