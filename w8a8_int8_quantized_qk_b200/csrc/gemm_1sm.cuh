@@ -61,7 +61,7 @@ __device__ __forceinline__ void teardown(S& s, uint32_t tmem) {
 // loads in flight together; integer adds, exact), then dequantises and
 // stores.  The scales of the whole tile were staged in the warp's slot
 // before the accumulator was ready.
-template <int BN, bool F8, class S>
+template <int BN, bool F8, bool SUMS, class S>
 __device__ void channel_cluster_reduce(S& s, const Args& p, const CUtensorMap* tmO) {
   const int lane = threadIdx.x & 31;
   const int ew = (threadIdx.x >> 5) - 2;
@@ -120,7 +120,7 @@ __device__ void channel_cluster_reduce(S& s, const Args& p, const CUtensorMap* t
     }
     if (!F8 && p.asym.zp) apply_zp(p, row, col0, va);
     if (p.tma_out)
-      store32_tma<F8>(p, tmO, box, row0, col0, sa, sws + c * 32, va);
+      store32_tma<F8, SUMS>(p, tmO, box, row0, col0, sa, sws + c * 32, va);
     else if (rv && col0 < p.n)
       store32_channel<F8>(p, row, col0, sa, sws + c * 32, va);
   }
@@ -162,7 +162,8 @@ struct alignas(1024) ChannelStorageT {
 };
 using ChannelStorage = ChannelStorageT<kChannelBN>;
 
-template <bool F8, bool MOE = false, int BN = kChannelBN>
+// SUMS: the int32 sums alone leave, by TMA stores (store32_tma).
+template <bool F8, bool MOE = false, int BN = kChannelBN, bool SUMS = false>
 __global__ void __launch_bounds__(kChannelThreads, 1)
     gemm_i8_channel_kernel(const __grid_constant__ CUtensorMap tmA,
                            const __grid_constant__ CUtensorMap tmB,
@@ -190,11 +191,11 @@ __global__ void __launch_bounds__(kChannelThreads, 1)
     if (lane == 0) mma_issue<BN, kStages, 2, false, F8, MOE>(s, tmem, p);
     __syncwarp();
   } else {
-    epilogue_channel<BN, 2, F8, MOE>(s, tmem, p, &tmO);
+    epilogue_channel<BN, 2, F8, MOE, SUMS>(s, tmem, p, &tmO);
   }
   if (p.sk.csplit) {
     cluster_sync_all();  // every CTA of the cluster has staged its partial
-    if (warp >= 2) channel_cluster_reduce<BN, F8>(s, p, &tmO);
+    if (warp >= 2) channel_cluster_reduce<BN, F8, SUMS>(s, p, &tmO);
     cluster_sync_all();  // the peers are done reading this CTA's slots
   }
   teardown(s, tmem);

@@ -505,22 +505,22 @@ __device__ __forceinline__ void store_box(const CUtensorMap* tmO, uint8_t* box, 
 // form): half the FMA-pipe instructions, which compete with the tensor
 // core's MMAs on the same SM (0.6 us of a 52 us prefill GEMM).  (Leaving
 // out the exact multiply by an output_scale of 1 measured no faster.)
-// With tma_out 2 the sums themselves are written, in two boxes of 16 columns:
+// SUMS (tma_out 2): the sums themselves are written, in two boxes of 16 columns:
 // 16-byte stores from registers fill half a 32-byte sector each (4096 x 4096 x 4096:
-// 63 us with those, 55 us so).
-template <bool F8 = false>
+// 67 us with those, 52 us so).  Kernels of their own write them: as a branch of one
+// kernel for both they slowed short GEMMs with bf16 outputs by 0.1 to 0.3 us (128 x 264 x
+// 528 4.6 -> 4.8 us, 2304 x 2304 x 512 8.3 -> 8.6 us).
+template <bool F8 = false, bool SUMS = false>
 __device__ __forceinline__ void store32_tma(const Args& p, const CUtensorMap* tmO, uint8_t* box,
                                             int row0, int col0, float sa, const float* sw,
                                             const uint32_t (&v)[32]) {
   if (col0 >= p.n || row0 >= p.m) return;  // the box lies wholly outside (warp-uniform)
   const int lane = threadIdx.x & 31;
-  if constexpr (!F8) {
-    if (p.tma_out == 2) {
+  if constexpr (SUMS) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (col0 + h * 16 < p.n) store_box(tmO, box, col0 + h * 16, row0, lane, v + h * 16);
-      return;
-    }
+    for (int h = 0; h < 2; ++h)
+      if (col0 + h * 16 < p.n) store_box(tmO, box, col0 + h * 16, row0, lane, v + h * 16);
+    return;
   }
   uint32_t w[16];
   const uint64_t sa2 = pack2(__float_as_uint(sa), __float_as_uint(sa));
@@ -547,7 +547,7 @@ __device__ __forceinline__ void store32_tma(const Args& p, const CUtensorMap* tm
 // row's token scale; the 32-column TMEM loads are double-buffered so the
 // next load is in flight while the current chunk is converted and stored.
 // bf16 output without c leaves through TMA stores (store32_tma).
-template <int BN, int NACC, bool F8 = false, bool MOE = false, class S>
+template <int BN, int NACC, bool F8 = false, bool MOE = false, bool SUMS = false, class S>
 __device__ void epilogue_channel(S& s, uint32_t tmem, const Args& p, const CUtensorMap* tmO) {
   const int nunits = p.tiles_m * p.tiles_n * p.sk.splits;
   const int lane = threadIdx.x & 31;
@@ -608,7 +608,7 @@ __device__ void epilogue_channel(S& s, uint32_t tmem, const Args& p, const CUten
       } else {
         if (p.asym.zp) apply_zp(p, row, colbase + ch * 32, v);
         if (p.tma_out)
-          store32_tma(p, tmO, box, row0, colbase + ch * 32, sa, sws + ch * 32, v);
+          store32_tma<false, SUMS>(p, tmO, box, row0, colbase + ch * 32, sa, sws + ch * 32, v);
         else if (rv)
           store32_channel(p, row, colbase + ch * 32, sa, sws + ch * 32, v);
       }

@@ -345,15 +345,15 @@ inline int launch_pair(Args a, const int8_t* A, const int8_t* B, int dev, int nu
   }
   const int ntiles = a.tiles_m * a.tiles_n * a.sk.splits;  // > pairs whenever the tail split is on
   const int grid_pairs = ntiles < pairs ? ntiles : pairs;
-  cudaError_t e = a.f8 ? set_smem_once(gemm_i8_pair_kernel<true>, dev, 4, pair_smem())
-                       : set_smem_once(gemm_i8_pair_kernel<false>, dev, 0, pair_smem());
+  auto* kernel = a.f8             ? gemm_i8_pair_kernel<true>
+                 : a.tma_out == 2 ? gemm_i8_pair_kernel<false, false, true>
+                                  : gemm_i8_pair_kernel<false>;
+  cudaError_t e = set_smem_once(kernel, dev, a.f8 ? 4 : (a.tma_out == 2 ? 12 : 0), pair_smem());
   if (e == cudaSuccess) {
     // cluster: one pair, or (cluster split-K) the splits pairs of one tile;
     // the grid is then exactly tiles x splits pairs, one unit each
     const unsigned cluster = pl.csplit ? 2u * static_cast<unsigned>(pl.splits) : 2u;
-    e = launch_pdl(a.f8 ? gemm_i8_pair_kernel<true> : gemm_i8_pair_kernel<false>, dim3(2 * grid_pairs),
-                   dim3(kPairThreads), pair_smem(), stream,
-                   cluster, ta, tb, to, a);
+    e = launch_pdl(kernel, dim3(2 * grid_pairs), dim3(kPairThreads), pair_smem(), stream, cluster, ta, tb, to, a);
   }
   *err = e;
   return e == cudaSuccess ? 0 : 2;
@@ -656,14 +656,18 @@ inline int launch(Args a, const int8_t* A, const int8_t* B, bool group, int dev,
     const unsigned cluster = a.sk.csplit ? static_cast<unsigned>(a.sk.splits) : 1u;
     if (bn == 128) {
       const size_t smem = channel_smem<128>();
-      auto* kernel = a.f8 ? gemm_i8_channel_kernel<true, false, 128> : gemm_i8_channel_kernel<false, false, 128>;
-      e = set_smem_once(kernel, dev, a.f8 ? 10 : 9, smem);
+      auto* kernel = a.f8             ? gemm_i8_channel_kernel<true, false, 128>
+                     : a.tma_out == 2 ? gemm_i8_channel_kernel<false, false, 128, true>
+                                      : gemm_i8_channel_kernel<false, false, 128>;
+      e = set_smem_once(kernel, dev, a.f8 ? 10 : (a.tma_out == 2 ? 13 : 9), smem);
       if (e == cudaSuccess)
         e = launch_pdl(kernel, dim3(grid), dim3(kChannelThreads), smem, stream, cluster, ta, tb, to, a);
     } else {
       const size_t smem = channel_smem();
-      auto* kernel = a.f8 ? gemm_i8_channel_kernel<true> : gemm_i8_channel_kernel<false>;
-      e = set_smem_once(kernel, dev, a.f8 ? 5 : 1, smem);
+      auto* kernel = a.f8             ? gemm_i8_channel_kernel<true>
+                     : a.tma_out == 2 ? gemm_i8_channel_kernel<false, false, kChannelBN, true>
+                                      : gemm_i8_channel_kernel<false>;
+      e = set_smem_once(kernel, dev, a.f8 ? 5 : (a.tma_out == 2 ? 14 : 1), smem);
       if (e == cudaSuccess)
         e = launch_pdl(kernel, dim3(grid), dim3(kChannelThreads), smem, stream, cluster, ta, tb, to, a);
     }

@@ -229,7 +229,7 @@ __device__ void mma_issue_pair(PairStorage& s, uint32_t tmem, const Args& p, uin
 // fixed order for fp32), runs the per-channel epilogue and resets the
 // counter.  No slice waits for another, and none holds its TMEM buffer
 // through the reduction.
-template <bool F8>
+template <bool F8, bool SUMS>
 __device__ void tail_slice_epilogue(uint32_t acc_empty_lead, const Args& p,
                                     const PairUnit& u, int region, uint32_t tb, int row, bool rv,
                                     float sa, int colbase, const float* sws,
@@ -293,7 +293,7 @@ __device__ void tail_slice_epilogue(uint32_t acc_empty_lead, const Args& p,
       }
     if (!F8 && p.asym.zp) apply_zp(p, row, colbase + ch * 32, va);
     if (p.tma_out)
-      store32_tma<F8>(p, tmO, box, row - lane, colbase + ch * 32, sa, sws + ch * 32, va);
+      store32_tma<F8, SUMS>(p, tmO, box, row - lane, colbase + ch * 32, sa, sws + ch * 32, va);
     else if (rv)
       store32_channel<F8>(p, row, colbase + ch * 32, sa, sws + ch * 32, va);
   }
@@ -307,7 +307,7 @@ __device__ void tail_slice_epilogue(uint32_t acc_empty_lead, const Args& p,
 // token scale is fetched before the accumulator is ready, and the four
 // 32-column TMEM loads are double-buffered so the next load is in flight
 // while the current chunk is converted and stored.
-template <bool F8, bool MOE>
+template <bool F8, bool MOE, bool SUMS>
 __device__ void epilogue_pair(PairStorage& s, uint32_t tmem, const Args& p, uint32_t pr,
                               uint32_t lead, const CUtensorMap* tmO) {
   const int npairs = gridDim.x >> 1;
@@ -352,8 +352,8 @@ __device__ void epilogue_pair(PairStorage& s, uint32_t tmem, const Args& p, uint
     uint32_t va[32], vb[32];
     if (tail) {
       // (releases the TMEM buffer itself, before its reduction)
-      tail_slice_epilogue<F8>(map_to_rank(smem_addr(&s.acc_empty[abuf]), lead), p, u, region,
-                              tb, row, rv, sa, colbase, sws, tmO, box);
+      tail_slice_epilogue<F8, SUMS>(map_to_rank(smem_addr(&s.acc_empty[abuf]), lead), p, u, region,
+                                    tb, row, rv, sa, colbase, sws, tmO, box);
     } else if (F8 && !p.sk.csplit) {
       // FP8 kind, whole tile (fp32 accumulator)
       auto emit = [&](int ch, const uint32_t(&v)[32]) {
@@ -380,11 +380,11 @@ __device__ void epilogue_pair(PairStorage& s, uint32_t tmem, const Args& p, uint
       for (int ch = 0; ch < 4; ch += 2) {
         tmem_ld_32x32b_x32(tb + (ch + 1) * 32, vb);
         if (p.asym.zp) apply_zp(p, row, colbase + ch * 32, va);
-        store32_tma(p, tmO, box, row - lane, colbase + ch * 32, sa, sws + ch * 32, va);
+        store32_tma<false, SUMS>(p, tmO, box, row - lane, colbase + ch * 32, sa, sws + ch * 32, va);
         tmem_ld_wait();
         if (ch + 2 < 4) tmem_ld_32x32b_x32(tb + (ch + 2) * 32, va);
         if (p.asym.zp) apply_zp(p, row, colbase + (ch + 1) * 32, vb);
-        store32_tma(p, tmO, box, row - lane, colbase + (ch + 1) * 32, sa, sws + (ch + 1) * 32, vb);
+        store32_tma<false, SUMS>(p, tmO, box, row - lane, colbase + (ch + 1) * 32, sa, sws + (ch + 1) * 32, vb);
         tmem_ld_wait();
       }
     } else if (p.sk.splits == 1) {
@@ -579,7 +579,8 @@ __device__ void cluster_reduce_pair(PairStorage& s, const Args& p, uint32_t cran
   }
 }
 
-template <bool F8, bool MOE = false>
+// SUMS: the int32 sums alone leave, by TMA stores (store32_tma).
+template <bool F8, bool MOE = false, bool SUMS = false>
 __global__ void __launch_bounds__(kPairThreads, 1)
     gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmB,
@@ -625,7 +626,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (lane == 0 && pr == 0) mma_issue_pair<F8, MOE>(s, tmem, p, lead);
     __syncwarp();
   } else {
-    epilogue_pair<F8, MOE>(s, tmem, p, pr, lead, &tmO);
+    epilogue_pair<F8, MOE, SUMS>(s, tmem, p, pr, lead, &tmO);
   }
   if (p.sk.csplit) {
     if (warp >= 2) cluster_reduce_scales(s, p, crank);
