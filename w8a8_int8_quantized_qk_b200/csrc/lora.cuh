@@ -259,7 +259,7 @@ __device__ __forceinline__ void load_x(const void* x, int64_t at, bool in, uint4
   const char* p = static_cast<const char*>(x) + at * (BF16 ? 2 : 4);
 #pragma unroll
   for (int i = 0; i < (BF16 ? 1 : 2); ++i)
-    v[i] = in ? ld_nc_v4(p + i * 16) : make_uint4(0, 0, 0, 0);
+    v[i] = in ? ld_nc_v4(p + i * 16) : vec4(0, 0, 0, 0);
 }
 template <bool BF16>
 __device__ __forceinline__ void terms_x(const uint4 (&v)[BF16 ? 1 : 2], uint32_t (&t)[4][BF16 ? 1 : 3]) {
@@ -318,8 +318,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_kernel(Args p) 
       load_x<BF16>(p.x, static_cast<int64_t>(tok1) * p.k + ku, tok1 >= 0 && in, x1[u]);
 #pragma unroll
       for (int j = 0; j < RT; ++j)
-        b[u][j] = (j * 8 < ranks && in) ? ld_nc_v4(a + static_cast<int64_t>(j * 8 + g) * p.k + ku)
-                                        : make_uint4(0, 0, 0, 0);
+        b[u][j] = (j * 8 < ranks && in) ? ld_nc_v4(a + static_cast<int64_t>(j * 8 + g) * p.k + ku) : vec4(0, 0, 0, 0);
     }
     // The instruction truncates as it accumulates: a batch's products are summed on
     // their own, the smallest terms first, and added to the rest with rounding (300
@@ -415,7 +414,7 @@ __device__ __forceinline__ void store8(const Args& p, int row, int col, const in
   const uint64_t o = static_cast<uint64_t>(static_cast<uint32_t>(row)) * static_cast<uint32_t>(p.n) + static_cast<uint32_t>(col);
   if (p.out_bf16) {
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + o) =
-        make_uint4(pack_bf16x2(v0, v1), pack_bf16x2(v2, v3), pack_bf16x2(v4, v5), pack_bf16x2(v6, v7));
+        vec4(pack_bf16x2(v0, v1), pack_bf16x2(v2, v3), pack_bf16x2(v4, v5), pack_bf16x2(v6, v7));
   } else {
     float4* out = reinterpret_cast<float4*>(static_cast<float*>(p.out) + o);
     out[0] = make_float4(v0, v1, v2, v3);
@@ -450,7 +449,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(Args p) 
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int r = st * 32 + q * 8, c = col0 + v * 256 + (g >> 1) * 8 + j * 2 + (g & 1);
-      bv[v][j] = (c < p.n && r < p.rank) ? ld_nc_v4(b + static_cast<int64_t>(c) * p.rank + r) : make_uint4(0, 0, 0, 0);
+      bv[v][j] = (c < p.n && r < p.rank) ? ld_nc_v4(b + static_cast<int64_t>(c) * p.rank + r) : vec4(0, 0, 0, 0);
     }
   };
   if (use >= 0) {
@@ -728,7 +727,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_long_kernel(Arg
             if constexpr (RK > 32) {
               cp_async16(smem_addr(bs) + (st * 4 + j) * kExpandThreads * 16, at, on);
             } else if constexpr (HALVES == 2) {
-              const uint4 v = on ? __ldg(reinterpret_cast<const uint4*>(at)) : make_uint4(0, 0, 0, 0);
+              const uint4 v = on ? __ldg(reinterpret_cast<const uint4*>(at)) : vec4(0, 0, 0, 0);
               bv[j][0] = v.x;
               bv[j][1] = v.y;
               bv[j][2] = v.z;

@@ -62,11 +62,9 @@ __device__ __forceinline__ uint4 ld_v4(const void* p) {
 template <bool BF16>
 __device__ __forceinline__ uint4 narrow(const float (&f)[BF16 ? 8 : 4]) {
   if constexpr (BF16) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
+    return vec4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
   } else {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                      __float_as_uint(f[3]));
+    return vec4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
   }
 }
 
@@ -190,7 +188,7 @@ __global__ void __launch_bounds__(quant::kMaxThreads) norm_quant_rows_kernel(Arg
   for (int j = 0; j < kRowVec; ++j) {
     const int v = t0 + j * stride;
     const int64_t o = static_cast<int64_t>(v) * 16;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const uint4 zero = vec4(0, 0, 0, 0);
     r[j] = v < nvec ? ld_v4(xr + o) : zero;
     w[j] = v < nvec ? ld_nc_v4(static_cast<const char*>(p.w) + o) : zero;
   }
@@ -199,7 +197,7 @@ __global__ void __launch_bounds__(quant::kMaxThreads) norm_quant_rows_kernel(Arg
 #pragma unroll
     for (int j = 0; j < kRowVec; ++j) {
       const int v = t0 + j * stride;
-      d[j] = v < nvec ? ld_v4(rr + static_cast<int64_t>(v) * 16) : make_uint4(0, 0, 0, 0);
+      d[j] = v < nvec ? ld_v4(rr + static_cast<int64_t>(v) * 16) : vec4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int j = 0; j < kRowVec; ++j) r[j] = add_rows<BF16>(r[j], d[j]);
@@ -257,13 +255,13 @@ __global__ void __launch_bounds__(T) norm_quant_persistent_kernel(Args p) {
     for (int j = 0; j < V; ++j) {
       const int v = tid + j * T;
       const bool in = row < p.m && v < nvec;
-      x[j] = in ? ld_v4(xr + static_cast<int64_t>(v) * 16) : make_uint4(0, 0, 0, 0);
-      if constexpr (RES) d[j] = in ? ld_v4(rr + static_cast<int64_t>(v) * 16) : make_uint4(0, 0, 0, 0);
+      x[j] = in ? ld_v4(xr + static_cast<int64_t>(v) * 16) : vec4(0, 0, 0, 0);
+      if constexpr (RES) d[j] = in ? ld_v4(rr + static_cast<int64_t>(v) * 16) : vec4(0, 0, 0, 0);
     }
   };
   auto weight = [&](int j) {
     const int v = tid + j * T;
-    return v < nvec ? __ldg(static_cast<const uint4*>(p.w) + v) : make_uint4(0, 0, 0, 0);
+    return v < nvec ? __ldg(static_cast<const uint4*>(p.w) + v) : vec4(0, 0, 0, 0);
   };
   fetch(xc, dc, blockIdx.x);
   if constexpr (KEEP) {
